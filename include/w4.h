@@ -379,6 +379,110 @@ w4_status w4a16_gemm_decode_static(const void *X, w4_dtype x_dtype, int64_t M,
 size_t w4a16_gemm_decode_static_capacity(void);
 
 /*
+ * Fused operators: the layer around the matmul, and its gradients.  The source
+ * pages name the fused dequantize-matmul only (ch. 22, section 22.3); these calls
+ * take the same weights and put what a transformer block does next into the same
+ * kernel, and give the gradients that training adapters over frozen 4-bit
+ * weights needs.  W^ is the [N][K] matrix of the rule above, act is one of:
+ */
+typedef enum {
+  W4_ACT_NONE = 0,     /* z */
+  W4_ACT_RELU = 1,     /* max(z, 0) */
+  W4_ACT_SILU = 2,     /* z / (1 + exp(-z)) */
+  W4_ACT_GELU = 3,     /* z (1 + erf(z / sqrt 2)) / 2 */
+  W4_ACT_GELU_TANH = 4 /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+} w4_act;
+
+/*
+ * Linear layer:  Z = X . W^T + bias,  Y = act(Z) + residual.
+ *   X         device [M][K], F16 or BF16
+ *   bias      device [N] fp32 or NULL
+ *   residual  device [M][N] of Y's type or NULL; Y itself may be given (the sum
+ *             is then formed in place)
+ *   Z         device [M][N] of X's type, or NULL: the pre-activations for the
+ *             backward pass (w4a16_linear_grad)
+ *   Y         device [M][N], F32, F16 or BF16
+ *   group     32, 64 or 128; K a multiple of the group and of 64
+ *   packed, scales, zeros, awq_s   as for w4a16_gemm
+ *   workspace device scratch of w4a16_linear_workspace_size(M, N, K) bytes, zero-
+ *             filled before its first use, under the same rule as w4a16_gemm's:
+ *             the first 128 KiB are left zero by every call, the rest holds nothing
+ *             between calls, and calls that share it must not overlap in time.
+ *             The operators of this header may share one workspace.
+ * Z is accumulated in fp32; bias, activation and residual are applied in fp32 and
+ * each output is rounded once.  W^ (and, with awq_s, x * s) may be rounded to fp16
+ * once before the product.  A token with an infinity or NaN among its activations
+ * gets non-finite or unspecified outputs; other tokens are not affected.
+ * Outputs may not overlap inputs (but Y = residual) or each other: refused with
+ * W4_ERR_INVALID_ARG.  Results do not depend on the order in which blocks finish.
+ */
+w4_status w4a16_linear(const void *X, w4_dtype x_dtype, int64_t M, int64_t N,
+                       int64_t K, int group, const uint8_t *packed,
+                       const uint16_t *scales, const uint16_t *zeros,
+                       const float *awq_s, const float *bias, w4_act act,
+                       const void *residual, void *Z, void *Y,
+                       w4_dtype y_dtype, void *workspace,
+                       size_t workspace_bytes, w4_stream_t stream);
+
+/*
+ * Gated feed-forward input:  [G U] = X . W^T + bias,  H = act(G) * U, in one kernel.
+ *   packed, scales, zeros   of the [2F][K] matrix: F gate rows, then F up rows
+ *   bias      device [2F] fp32 or NULL
+ *   Z         device [M][2F] of X's type, or NULL: G and U for w4a16_gated_grad
+ *   H         device [M][F], F32, F16 or BF16
+ * Otherwise as w4a16_linear.  The block's down projection is a w4a16_linear of H.
+ */
+w4_status w4a16_gated(const void *X, w4_dtype x_dtype, int64_t M, int64_t F,
+                      int64_t K, int group, const uint8_t *packed,
+                      const uint16_t *scales, const uint16_t *zeros,
+                      const float *awq_s, const float *bias, w4_act act,
+                      void *Z, void *H, w4_dtype h_dtype, void *workspace,
+                      size_t workspace_bytes, w4_stream_t stream);
+
+/*
+ * Gradient of w4a16_linear for frozen weights:
+ *   dZ = dY * act'(Z),  dX = dZ . W^,  dbias[n] = sum over m of dZ[m][n].
+ * (The residual's gradient is dY itself.)
+ *   dY        device [M][N], F16 or BF16
+ *   Z         device [M][N] of dY's type: the pre-activations; may be NULL with
+ *             W4_ACT_NONE
+ *   dX        device [M][K], F32, F16 or BF16
+ *   dbias     device [N] fp32, or NULL
+ * dZ is formed in fp32 and rounded to fp16 once, with a power of two per token, for
+ * the product; dbias sums the fp32 values.  Workspace, refusals, non-finite values
+ * and the rest as for w4a16_linear.
+ */
+w4_status w4a16_linear_grad(const void *dY, w4_dtype dy_dtype, int64_t M,
+                            int64_t N, int64_t K, int group,
+                            const uint8_t *packed, const uint16_t *scales,
+                            const uint16_t *zeros, const float *awq_s,
+                            const void *Z, w4_act act, void *dX,
+                            w4_dtype dx_dtype, float *dbias, void *workspace,
+                            size_t workspace_bytes, w4_stream_t stream);
+
+/*
+ * Gradient of w4a16_gated for frozen weights, from the saved Z = [G U]:
+ *   dG = dH * U * act'(G),  dU = dH * act(G),  dX = [dG dU] . W^,
+ *   dbias [2F] = sums of [dG dU] over the tokens.
+ *   dH        device [M][F], F16 or BF16;  Z device [M][2F] of dH's type
+ * Otherwise as w4a16_linear_grad.
+ */
+w4_status w4a16_gated_grad(const void *dH, w4_dtype dh_dtype, int64_t M,
+                           int64_t F, int64_t K, int group,
+                           const uint8_t *packed, const uint16_t *scales,
+                           const uint16_t *zeros, const float *awq_s,
+                           const void *Z, w4_act act, void *dX,
+                           w4_dtype dx_dtype, float *dbias, void *workspace,
+                           size_t workspace_bytes, w4_stream_t stream);
+
+/* Bytes of workspace the fused operators need for these sizes, whatever the
+ * group, types and optional arguments (0 for invalid sizes). */
+size_t w4a16_linear_workspace_size(int64_t M, int64_t N, int64_t K);
+size_t w4a16_gated_workspace_size(int64_t M, int64_t F, int64_t K);
+size_t w4a16_linear_grad_workspace_size(int64_t M, int64_t N, int64_t K);
+size_t w4a16_gated_grad_workspace_size(int64_t M, int64_t F, int64_t K);
+
+/*
  * Device-side error word: kernels whose bounded waits run out set it instead
  * of hanging.  Copies its value to *flag (0 = no error) and clears it; this
  * call synchronizes the current device.  Library error reporting: the pages

@@ -1,0 +1,74 @@
+// act.cuh -- the activations of the fused operators and their derivatives, in fp32.
+//
+// SiLU and tanh-GELU are both x times the logistic function of 2u (u = x / 2, or
+// u = sqrt(2/pi) (x + 0.044715 x^3)), which has no cancellation for negative x the
+// way 1 + tanh(u) has.  NaN stays NaN in every one of them.
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace w4 {
+
+enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
+
+constexpr float kSqrt2OverPi = 0.7978845608028654f;
+constexpr float kGeluCubic = 0.044715f;
+
+// 1 / (1 + exp(-v)); exp overflows to infinity for v < -88, which gives 0 as it should.
+__device__ __forceinline__ float logistic(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+
+__device__ __forceinline__ float act_fwd(float x, int act) {
+  switch (act) {
+    case kActRelu: return x < 0.0f ? 0.0f : x;
+    case kActSilu: return x * logistic(x);
+    case kActGelu: return 0.5f * x * erfcf(-0.7071067811865476f * x);
+    case kActGeluTanh: return x * logistic(2.0f * kSqrt2OverPi * (x + kGeluCubic * x * x * x));
+    default: return x;
+  }
+}
+
+// act(x) and act'(x)
+__device__ __forceinline__ void act_both(float x, int act, float &y, float &dy) {
+  switch (act) {
+    case kActRelu:
+      y = x < 0.0f ? 0.0f : x;
+      dy = x > 0.0f ? 1.0f : (x <= 0.0f ? 0.0f : x);  // NaN stays NaN
+      break;
+    case kActSilu: {
+      const float s = logistic(x);
+      y = x * s;
+      dy = s + y * logistic(-x);  // s (1 + x (1 - s)), 1 - s = logistic(-x)
+      break;
+    }
+    case kActGelu: {
+      const float c = 0.5f * erfcf(-0.7071067811865476f * x);
+      y = x * c;
+      dy = c + x * 0.3989422804014327f * __expf(-0.5f * x * x);
+      break;
+    }
+    case kActGeluTanh: {
+      const float v = 2.0f * kSqrt2OverPi * (x + kGeluCubic * x * x * x);
+      const float s = logistic(v);
+      y = x * s;
+      dy = s + y * logistic(-v) * 2.0f * kSqrt2OverPi * (1.0f + 3.0f * kGeluCubic * x * x);
+      break;
+    }
+    default:
+      y = x;
+      dy = 1.0f;
+  }
+}
+
+// 16- and 32-bit elements by w4_dtype number (0 fp32, 1 fp16, 2 bf16)
+__device__ __forceinline__ float load_as_float(const void *p, int dtype, int64_t i) {
+  if (dtype == 0) return static_cast<const float *>(p)[i];
+  if (dtype == 1) return __half2float(static_cast<const __half *>(p)[i]);
+  return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+}
+__device__ __forceinline__ void store_from_float(void *p, int dtype, int64_t i, float v) {
+  if (dtype == 0) static_cast<float *>(p)[i] = v;
+  else if (dtype == 1) static_cast<__half *>(p)[i] = __float2half_rn(v);
+  else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+}
+
+}  // namespace w4

@@ -23,6 +23,7 @@
 #include "awq_search.cu"
 #include "outliers.cu"
 #include "gptq.cu"
+#include "fused_simple.cu"
 #include "w4.h"
 
 namespace w4 {
@@ -1192,3 +1193,5 @@ w4_status w4_quantize_gptq(const float *W, int64_t N, int64_t K, int group, cons
 }
 
 }  // extern "C"
+
+#include "fused_api.cu"

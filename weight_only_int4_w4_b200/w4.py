@@ -7,6 +7,7 @@ not built, importing this module raises.
 
 Names follow the C ABI: ``w4_quantize`` (and ``w4_quantize_symmetric``), ``w4_pack``, ``w4a16_gemm``,
 ``w4a16_gemm_workspace_size``, ``w4a16_gemm_host``, ``w4a16_gemm_decode_static``,
+``w4a16_linear``, ``w4a16_gated``, ``w4a16_linear_grad``, ``w4a16_gated_grad``,
 ``w4_device_error``.
 """
 from __future__ import annotations
@@ -53,6 +54,17 @@ _lib.w4_gptq_workspace_size.argtypes = [_I64, _I64]
 _lib.w4_gptq_workspace_size.restype = _SZ
 _lib.w4a16_gemm_workspace_size.argtypes = [_I64, _I64, _I64]
 _lib.w4a16_gemm_workspace_size.restype = _SZ
+
+
+_I = ctypes.c_int
+_lib.w4a16_linear.argtypes = [_P, _I, _I64, _I64, _I64, _I, _P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _P, _SZ, _P]
+_lib.w4a16_gated.argtypes = [_P, _I, _I64, _I64, _I64, _I, _P, _P, _P, _P, _P, _I, _P, _P, _I, _P, _SZ, _P]
+_lib.w4a16_linear_grad.argtypes = [_P, _I, _I64, _I64, _I64, _I, _P, _P, _P, _P, _P, _I, _P, _I, _P, _P, _SZ, _P]
+_lib.w4a16_gated_grad.argtypes = _lib.w4a16_linear_grad.argtypes
+for _f in ("w4a16_linear", "w4a16_gated", "w4a16_linear_grad", "w4a16_gated_grad"):
+    getattr(_lib, _f).restype = _I
+    getattr(_lib, _f + "_workspace_size").argtypes = [_I64, _I64, _I64]
+    getattr(_lib, _f + "_workspace_size").restype = _SZ
 
 
 class GemmItem(ctypes.Structure):
@@ -340,6 +352,194 @@ def w4_awq_search(W: torch.Tensor, Xcal: torch.Tensor, alphas=AWQ_EXPONENTS, gro
                               _ptr(s), ctypes.cast(errs, _P), ctypes.cast(ctypes.pointer(best), _P), _ptr(ws),
                               ws.numel(), _stream(stream)), "w4_awq_search")
     return s, alphas[best.value], list(errs)
+
+
+# ---------------------------------------------------------------- fused operators
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}  # w4_act of include/w4.h
+_COUNTER_BYTES = 128 * 1024  # the part of a workspace that is zero before and after every call
+
+
+def w4a16_linear_workspace_size(M: int, N: int, K: int) -> int:
+    return int(_lib.w4a16_linear_workspace_size(M, N, K))
+
+
+def w4a16_gated_workspace_size(M: int, F: int, K: int) -> int:
+    return int(_lib.w4a16_gated_workspace_size(M, F, K))
+
+
+def w4a16_linear_grad_workspace_size(M: int, N: int, K: int) -> int:
+    return int(_lib.w4a16_linear_grad_workspace_size(M, N, K))
+
+
+def w4a16_gated_grad_workspace_size(M: int, F: int, K: int) -> int:
+    return int(_lib.w4a16_gated_grad_workspace_size(M, F, K))
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _fused_workspace(need: int, dev, raw_stream: int, stream):
+    """Scratch for one fused call on this stream: cached per device and stream, like
+    workspace(); while the stream is being captured into a graph, a buffer of the graph's
+    own (its counters are zeroed by the graph), so that no two graphs share one."""
+    if need == 0:
+        return None
+    capturing = torch.cuda.is_current_stream_capturing()
+    key = (dev, raw_stream)
+    buf = None if capturing else _fused_ws.get(key)
+    if buf is None or buf.numel() < need:
+        with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev):
+            buf = torch.empty(max(need, 1 << 20), dtype=torch.uint8, device=dev)
+            buf[:_COUNTER_BYTES].zero_()
+        if not capturing:
+            _fused_ws[key] = buf
+    return buf
+
+
+_fused_ws: dict = {}
+
+
+def _fused(name, X, out_cols, packed, scales, zeros, awq_s, group, act, out, out_dtype, ws, stream, extra):
+    """Checks what every fused call has in common, and makes it.  `extra(M, N, K)` gives the
+    call's own tensors (after checking them): the arguments between awq_s and out, and
+    those after out's type."""
+    _need(X.is_cuda and X.dim() == 2 and X.is_contiguous() and X.dtype in (torch.float16, torch.bfloat16),
+          f"{name}: the activations or gradients are a contiguous 2-D CUDA tensor in fp16 or bf16")
+    _need(packed.dim() == 2 and packed.dtype == torch.uint8 and packed.is_contiguous(), f"{name}: packed is uint8 [N, K/2]")
+    _need(act in ACTS, f"{name}: act is one of {sorted(ACTS)}")
+    _need(isinstance(group, int) and group > 0, f"{name}: group is a positive number")
+    M, dev = X.shape[0], X.device
+    N, K = packed.shape[0], packed.shape[1] * 2
+    for t, what in ((scales, "scales"), (zeros, "zeros")):
+        _need(t.dtype == torch.float16 and t.shape == (N, K // group) and t.is_contiguous(),
+              f"{name}: {what} is fp16 [N, K/group]")
+    if awq_s is not None:
+        _need(awq_s.dtype == torch.float32 and awq_s.shape == (K,) and awq_s.is_contiguous(), f"{name}: awq_s is fp32 [K]")
+    cols = out_cols(N, K)
+    if out is None:
+        out = torch.empty((M, cols), dtype=X.dtype if out_dtype is None else out_dtype, device=dev)
+    else:
+        _need(out.shape == (M, cols) and out.is_contiguous() and out_dtype in (None, out.dtype),
+              f"{name}: out is a contiguous [{M}, {cols}] tensor")
+    _need(out.dtype in _DT, f"{name}: output in fp32, fp16 or bf16")
+    mid, after, given = extra(M, N, K, out.dtype)
+    for t in (packed, scales, zeros, awq_s, out, ws, *given):
+        _need(t is None or t.device == dev, f"{name}: all tensors are on {dev}")
+    _need(ws is None or (ws.dtype == torch.uint8 and ws.is_contiguous()), f"{name}: ws is a contiguous uint8 tensor")
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _fused_call(name, X, M, N, K, group, packed, scales, zeros, awq_s, mid, out, after, ws, stream)
+    return _fused_call(name, X, M, N, K, group, packed, scales, zeros, awq_s, mid, out, after, ws, stream)
+
+
+def _fused_call(name, X, M, N, K, group, packed, scales, zeros, awq_s, mid, out, after, ws, stream):
+    dev = X.device
+    raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
+    rows = N // 2 if "gated" in name else N
+    if ws is None:
+        ws = _fused_workspace(getattr(_lib, name + "_workspace_size")(M, rows, K), dev, raw, stream)
+    _check(getattr(_lib, name)(X.data_ptr(), _DT[X.dtype], M, rows, K, group, packed.data_ptr(), scales.data_ptr(),
+                               zeros.data_ptr(), 0 if awq_s is None else awq_s.data_ptr(), *mid, out.data_ptr(),
+                               _DT[out.dtype], *after, 0 if ws is None else ws.data_ptr(),
+                               0 if ws is None else ws.numel(), raw), name)
+    return out
+
+
+def _opt(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _check_vec(name, what, t, n):
+    _need(t is None or (t.dtype == torch.float32 and t.shape == (n,) and t.is_contiguous()), f"{name}: {what} is fp32 [{n}]")
+
+
+def _check_mat(name, what, t, shape, dtype):
+    _need(t is None or (t.dtype == dtype and t.shape == shape and t.is_contiguous()),
+          f"{name}: {what} is a contiguous {dtype} tensor of shape {shape}")
+
+
+def w4a16_linear(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
+                 awq_s: torch.Tensor | None = None, bias: torch.Tensor | None = None, act: str = "none",
+                 residual: torch.Tensor | None = None, out_dtype=None, out: torch.Tensor | None = None,
+                 save_preact: bool = False, group: int = GROUP, ws: torch.Tensor | None = None, stream=None):
+    """Y = act(X . W^T + bias) + residual.  X [M,K] fp16/bf16 (CUDA), bias fp32 [N], residual [M,N] of
+    the output's type (`out` may be the residual itself); Y in out_dtype (X's type by default).
+    With save_preact, returns (Y, Z), Z = X . W^T + bias in X's type, for w4a16_linear_grad."""
+    Z = None
+
+    def extra(M, N, K, odt):
+        nonlocal Z
+        _need(X.shape[1] == K, f"w4a16_linear: X has {X.shape[1]} channels, the weights {K}")
+        _check_vec("w4a16_linear", "bias", bias, N)
+        _check_mat("w4a16_linear", "residual", residual, (M, N), odt)
+        if save_preact:
+            Z = torch.empty((M, N), dtype=X.dtype, device=X.device)
+        return (_opt(bias), ACTS[act], _opt(residual), _opt(Z)), (), (bias, residual)
+
+    Y = _fused("w4a16_linear", X, lambda N, K: N, packed, scales, zeros, awq_s, group, act, out, out_dtype, ws, stream,
+               extra)
+    return (Y, Z) if save_preact else Y
+
+
+def w4a16_gated(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
+                awq_s: torch.Tensor | None = None, bias: torch.Tensor | None = None, act: str = "silu", out_dtype=None,
+                out: torch.Tensor | None = None, save_preact: bool = False, group: int = GROUP,
+                ws: torch.Tensor | None = None, stream=None):
+    """H = act(G) * U with [G U] = X . W^T + bias; the weights' rows are F gate rows, then F up rows.
+    H [M,F] in out_dtype (X's type by default).  With save_preact, returns (H, Z), Z = [G U]
+    [M,2F] in X's type, for w4a16_gated_grad."""
+    Z = None
+
+    def extra(M, N, K, odt):
+        nonlocal Z
+        _need(N % 2 == 0, "w4a16_gated: the weights have an even number of rows, gate rows first")
+        _need(X.shape[1] == K, f"w4a16_gated: X has {X.shape[1]} channels, the weights {K}")
+        _check_vec("w4a16_gated", "bias", bias, N)
+        if save_preact:
+            Z = torch.empty((M, N), dtype=X.dtype, device=X.device)
+        return (_opt(bias), ACTS[act], _opt(Z)), (), (bias,)
+
+    H = _fused("w4a16_gated", X, lambda N, K: N // 2, packed, scales, zeros, awq_s, group, act, out, out_dtype, ws,
+               stream, extra)
+    return (H, Z) if save_preact else H
+
+
+def w4a16_linear_grad(dY: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
+                      awq_s: torch.Tensor | None = None, preact: torch.Tensor | None = None, act: str = "none",
+                      dbias: bool = False, out_dtype=None, out: torch.Tensor | None = None, group: int = GROUP,
+                      ws: torch.Tensor | None = None, stream=None):
+    """dX [M,K] = (dY * act'(Z)) . W^ for frozen weights.  dY [M,N] fp16/bf16 (CUDA), preact = Z [M,N] of
+    its type (not needed for act "none").  With dbias, returns (dX, dbias fp32 [N])."""
+    return _grad("w4a16_linear_grad", dY, lambda N: N, packed, scales, zeros, awq_s, preact, act, dbias, out_dtype,
+                 out, group, ws, stream)
+
+
+def w4a16_gated_grad(dH: torch.Tensor, preact: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
+                     zeros: torch.Tensor, awq_s: torch.Tensor | None = None, act: str = "silu", dbias: bool = False,
+                     out_dtype=None, out: torch.Tensor | None = None, group: int = GROUP,
+                     ws: torch.Tensor | None = None, stream=None):
+    """dX [M,K] = [dG dU] . W^ with dG = dH * U * act'(G), dU = dH * act(G), from preact = [G U] [M,2F] of
+    dH's type.  With dbias, returns (dX, dbias fp32 [2F])."""
+    return _grad("w4a16_gated_grad", dH, lambda N: N // 2, packed, scales, zeros, awq_s, preact, act, dbias, out_dtype,
+                 out, group, ws, stream)
+
+
+def _grad(name, dY, width, packed, scales, zeros, awq_s, preact, act, dbias, out_dtype, out, group, ws, stream):
+    db = None
+
+    def extra(M, N, K, odt):
+        nonlocal db
+        _need(N % 2 == 0 or name != "w4a16_gated_grad", f"{name}: the weights have an even number of rows, gate rows first")
+        _need(dY.shape[1] == width(N), f"{name}: the gradient has {dY.shape[1]} channels, the weights give {width(N)}")
+        _check_mat(name, "preact", preact, (M, N), dY.dtype)
+        if dbias:
+            db = torch.empty(N, dtype=torch.float32, device=dY.device)
+        return (_opt(preact), ACTS[act]), (_opt(db),), (preact,)
+
+    dX = _fused(name, dY, lambda N, K: K, packed, scales, zeros, awq_s, group, act, out, out_dtype, ws, stream, extra)
+    return (dX, db) if dbias else dX
 
 
 def w4_device_error() -> int:
