@@ -311,6 +311,30 @@ def test_same_bits_again_and_rows_behind_left_alone(w4, M):
         assert (b[:256] == 7).all() and (b[256 + n:] == 7).all()
 
 
+@pytest.mark.parametrize("op", ["linear", "gated", "linear_grad", "gated_grad"])
+def test_same_bits_under_load(w4, op):
+    """Many tiles per block, several runs with nothing between them: the same bits each time
+    (a buffer handed on too early shows here), and the 2-norm of the error."""
+    M, N, K = 1024, 8192, 4096
+    L = Layer(w4, N, K, seed=9)
+    if op in ("linear", "gated"):
+        X = L.randn(M, K).to(torch.bfloat16)
+        call = (lambda: w4.w4a16_linear(X, *L.w)) if op == "linear" else (lambda: w4.w4a16_gated(X, *L.w))
+        Z = L.z64(X, None)
+        ref = Z if op == "linear" else act64(Z[:, :N // 2], "silu") * Z[:, N // 2:]
+    else:
+        gated = op == "gated_grad"
+        dY = L.randn(M, N // 2 if gated else N).to(torch.bfloat16)
+        Z = L.randn(M, N).to(torch.bfloat16)
+        call = (lambda: w4.w4a16_gated_grad(dY, Z, *L.w)) if gated else \
+            (lambda: w4.w4a16_linear_grad(dY, *L.w, preact=Z, act="silu"))
+        ref = grad_ref(L, dY, Z, "silu", gated)[0] @ L.What
+    outs = [call() for _ in range(8)]
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
+    assert float((outs[0].double() - ref).norm() / ref.norm()) <= 3 * U + half_ulp(torch.bfloat16)
+
+
 @pytest.mark.parametrize("M", [2, 20, 90])
 def test_sizes_far_from_one(w4, M):
     """Weights from subnormal fp16 scales to the largest, groups of very different scale in

@@ -32,16 +32,65 @@ int64_t gated_rows(int64_t F) { return F < 1 || F > INT32_MAX / 2 ? 0 : 2 * F; }
 
 size_t dtype_size(w4_dtype t) { return t == W4_F32 ? 4 : 2; }
 
+// Launch plan and workspace of a fused call.
+struct FusedPlan {
+  int bn = 16, mt = 1, rt = 1, units = 1, gt = 1, full = 0, tiles = 1, tail_ctas = 0, grid = 1;
+  int64_t ld = 0;  // row stride of the staged operand
+  size_t xp = 0, tokf = 0, rowf = 0, part = 0, dbias = 0, bytes = 0;
+};
+
+// Fragments of a cut tile hold at least this many 128-deep units.
+constexpr int64_t kMinTailUnits = 4;
+
+// sizes whose tiles or blocks would not fit a grid are refused (false)
+bool fused_plan(int64_t M, int64_t N, int64_t K, bool gated, bool grad, int sm, FusedPlan &p) {
+  const int64_t rows = grad ? K : gated ? N / 2 : N, depth = grad ? N : K;
+  const int64_t mt = cdiv(M, w4::ftc::kMaxBn), rt = cdiv(rows, gated && !grad ? 64 : 128), units = cdiv(depth, 128);
+  if (M > (int64_t)1 << 30 || (double)rt * (double)mt > 1.0e9) return false;
+  p.mt = (int)mt;
+  p.bn = (int)(cdiv(cdiv(M, mt), 16) * 16);
+  p.rt = (int)rt;
+  p.units = (int)units;
+  p.gt = (int)std::min<int64_t>(mt, 8);
+  p.tiles = (int)(rt * mt);
+  p.full = p.tiles / sm * sm;
+  const int64_t rest = p.tiles - p.full;
+  if (rest > 0) {
+    const int64_t ctas = std::min<int64_t>(sm, rest * units / kMinTailUnits);
+    if (ctas > rest && rest * 10 < 9 * (int64_t)sm) p.tail_ctas = (int)ctas;
+    else p.full = p.tiles;
+  }
+  p.grid = p.full > 0 ? std::min(sm, std::max(p.full, p.tail_ctas)) : p.tail_ctas;
+  p.ld = grad ? cdiv(N, 8) * 8 : K;
+  p.xp = kCounterBytes;
+  p.tokf = p.xp + align256((size_t)M * p.ld * 2);
+  p.rowf = p.tokf + align256((size_t)M * 8);
+  p.part = p.rowf + align256((size_t)N * 8);
+  p.dbias = p.part + align256((size_t)2 * p.tail_ctas * p.bn * 128 * 4);
+  const size_t db = !grad ? 0
+                          : (size_t)std::max(w4::fused_dbias_ranges(M, N, true), w4::fused_dbias_ranges(M, N, false)) * N * 4;
+  p.bytes = p.dbias + align256(db);
+  return true;
+}
+
+int sm_count_or_b200() {
+  int sm = 0;
+  return current_sm_count(&sm) == cudaSuccess ? sm : 148;
+}
+
 size_t fused_ws_bytes(int64_t M, int64_t N, int64_t K, bool gated, bool grad) {
-  (void)K;
-  (void)gated;
-  return grad ? kCounterBytes + (size_t)M * N * 4 : 0;
+  FusedPlan p;
+  return fused_plan(M, N, K, gated, grad, sm_count_or_b200(), p) ? p.bytes : 0;
 }
 
 // Everything a fused call can be refused for, checked on the host.
 w4_status fused_check(const FusedCall &c) {
   w4_status st = check_shape(c.M, c.N, c.K, c.group);
   if (st != W4_OK) return st;
+  FusedPlan plan;
+  if (!fused_plan(c.M, c.N, c.K, c.gated, c.grad, sm_count_or_b200(), plan))
+    return fail(W4_ERR_INVALID_ARG, "M=%lld N=%lld K=%lld: too many tiles for one launch", (long long)c.M, (long long)c.N,
+                (long long)c.K);
   if (c.K % 64 != 0) return fail(W4_ERR_UNSUPPORTED, "K=%lld must be a multiple of 64", (long long)c.K);
   if (c.x_dtype != W4_F16 && c.x_dtype != W4_BF16)
     return fail(W4_ERR_UNSUPPORTED, "%s dtype must be F16 or BF16", c.grad ? "gradient" : "activation");
@@ -86,24 +135,67 @@ w4_status fused_check(const FusedCall &c) {
   return W4_OK;
 }
 
+// The tensor-core path: operand staging, the product, and the sum of cut tiles.
+w4_status fused_run_tc(const FusedCall &c, const FusedPlan &plan, cudaStream_t s) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+  if (!enc) return fail(W4_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  uint8_t *ws = static_cast<uint8_t *>(c.workspace);
+  uint16_t *xp = reinterpret_cast<uint16_t *>(ws + plan.xp);
+  float2 *tokf = reinterpret_cast<float2 *>(ws + plan.tokf), *rowf = reinterpret_cast<float2 *>(ws + plan.rowf);
+  const int64_t kg = c.K / c.group, depth = c.grad ? plan.ld : c.K;
+  CUtensorMap tmX, tmP;
+  CUresult r = encode_2d(enc, &tmX, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xp, (uint64_t)depth, (uint64_t)c.M,
+                         (uint64_t)plan.ld * 2, 64u, (uint32_t)plan.bn, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+  if (r != CUDA_SUCCESS) return fail(W4_ERR_CUDA, "tensor map for staged operands failed (CUresult %d)", (int)r);
+  r = encode_2d(enc, &tmP, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.packed, (uint64_t)(c.K / 2), (uint64_t)c.N,
+                (uint64_t)(c.K / 2), 64u, c.gated && !c.grad ? 64u : 128u, CU_TENSOR_MAP_SWIZZLE_64B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+  if (r != CUDA_SUCCESS) return fail(W4_ERR_CUDA, "tensor map for packed weights failed (CUresult %d)", (int)r);
+  cudaError_t e;
+  if (c.grad) {
+    if (c.dbias) {
+      e = w4::launch_fused_dbias(c.X, c.Z, (int)c.x_dtype, (int)c.act, c.gated, c.M, c.N,
+                                 reinterpret_cast<float *>(ws + plan.dbias), c.dbias, s);
+      if (e != cudaSuccess) return cuda_fail(e, "bias gradient launch");
+    }
+    e = w4::launch_fused_stage_dz(c.X, c.act == W4_ACT_NONE && !c.gated ? nullptr : c.Z, (int)c.x_dtype, (int)c.act,
+                                  c.gated, c.M, c.N, plan.ld, c.scales, kg, xp, tokf, rowf, s);
+  } else {
+    e = w4::launch_fused_stage_x(c.X, c.x_dtype == W4_BF16, c.awq_s, c.M, c.K, c.scales, kg, c.N, xp, tokf, rowf, s);
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "operand staging launch");
+  w4::FusedTcParams p{};
+  p.epi.M = c.M;
+  p.epi.N = c.grad ? c.K : c.gated ? c.N / 2 : c.N;
+  p.epi.rowf = rowf; p.epi.tokf = tokf;
+  p.epi.bias = c.bias;
+  p.epi.colmul = c.grad ? c.awq_s : nullptr;
+  p.epi.residual = c.residual; p.epi.Z = c.grad ? nullptr : c.Z; p.epi.Y = c.Y;
+  p.epi.act = c.grad ? (int)W4_ACT_NONE : (int)c.act;
+  p.epi.z_dtype = (int)c.x_dtype; p.epi.y_dtype = (int)c.y_dtype;
+  p.epi.vec = p.epi.N % 8 == 0;
+  p.scales = c.scales; p.zeros = c.zeros;
+  p.rows = c.N; p.kg = kg;
+  p.gshift = c.group == 128 ? 7 : c.group == 64 ? 6 : 5;
+  p.bn = plan.bn; p.mt = plan.mt; p.rt = plan.rt; p.units = plan.units; p.gt = plan.gt;
+  p.full = plan.full; p.tiles = plan.tiles; p.tail_ctas = plan.tail_ctas;
+  p.part = reinterpret_cast<float *>(ws + plan.part);
+  e = w4::launch_fused_tc(c.grad ? w4::kGrad : c.gated ? w4::kGated : w4::kLinear, tmX, tmP, p, plan.grid, s);
+  if (e != cudaSuccess) return cuda_fail(e, "fused product launch");
+  return W4_OK;
+}
+
 w4_status fused_run(const FusedCall &c, w4_stream_t stream) {
   t_last_error.clear();
   const w4_status st = fused_check(c);
   if (st != W4_OK) return st;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  w4::FusedParams p{};
-  p.X = c.X; p.x_dtype = (int)c.x_dtype;
-  p.M = c.M; p.N = c.N; p.K = c.K; p.group = c.group;
-  p.packed = c.packed; p.scales = c.scales; p.zeros = c.zeros; p.awq_s = c.awq_s; p.bias = c.bias;
-  p.act = (int)c.act; p.residual = c.residual; p.Z = c.Z; p.Y = c.Y; p.y_dtype = (int)c.y_dtype;
-  cudaError_t e;
-  if (!c.grad) e = w4::launch_fused_simple(p, c.gated, s);
-  else
-    e = w4::launch_fused_grad_simple(p, c.gated, c.X, c.Z,
-                                     reinterpret_cast<float *>(static_cast<uint8_t *>(c.workspace) + kCounterBytes),
-                                     c.dbias, s);
-  if (e != cudaSuccess) return cuda_fail(e, "fused operator launch");
-  return W4_OK;
+  int sm = 0;
+  cudaError_t e = current_sm_count(&sm);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  FusedPlan plan;
+  fused_plan(c.M, c.N, c.K, c.gated, c.grad, sm, plan);
+  return fused_run_tc(c, plan, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t fused_ws_query(int64_t M, int64_t N, int64_t K, bool gated, bool grad) {

@@ -1,0 +1,308 @@
+// fused_stage.cu -- operand preparation of the fused tensor-core products, and dbias.
+//
+// The products run on fp16 operands with powers of two taken out, so that neither side
+// can leave fp16's range and no bits but the last rounding are lost:
+//   rows    r[n] = 2^a with a such that the row's largest scale * r lies in [2^10, 2^11):
+//           (q - z) * (scale r) is at most 15 * 2^11 < 65504, and full precision reaches
+//           down to groups whose scale is 2^-24 of the row's largest.
+//   tokens  e[m] = 2^b with the token's largest |value| * e in [2^13, 2^14).
+// Both are undone in fp32 in the product's epilogue.  bf16 activations convert exactly
+// (8 significant bits); with AWQ, x * s is rounded to fp16 once.
+#include "act.cuh"
+#include "common.cuh"
+
+namespace w4 {
+
+// 2^k as a float, k in [-149, 127]
+__device__ __forceinline__ float pow2f(int k) {
+  return k >= -126 ? __uint_as_float((uint32_t)(k + 127) << 23) : __uint_as_float(1u << (k + 149));
+}
+
+// The factor 2^b that brings `amax` into [2^t, 2^(t+1)), and its inverse.  0, infinity
+// and NaN get 1 (a token with a non-finite value has non-finite outputs anyway).
+__device__ __forceinline__ float2 pow2_to(float amax, int t) {
+  if (!(amax > 0.0f) || amax > 3.4028235e38f) return make_float2(1.0f, 1.0f);
+  int b = t - ilogbf(amax);
+  b = b > 126 ? 126 : b;  // subnormal amax: 2^126 is enough to keep its few bits
+  return make_float2(pow2f(b), pow2f(-b));
+}
+
+__device__ __forceinline__ float block_max(float v, float *red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = red[0];
+  for (unsigned i = 1; i < blockDim.x / 32; ++i) v = fmaxf(v, red[i]);
+  return v;
+}
+
+// One warp: the row factors (r, 1 / r) of packed row n.
+__device__ __forceinline__ void row_factor(const uint16_t *scales, int64_t kg, int64_t n, float2 *rowf) {
+  const int lane = threadIdx.x & 31;
+  float mx = 0.0f;
+  for (int64_t g = lane; g < kg; g += 32) mx = fmaxf(mx, half_bits_to_float(scales[n * kg + g]));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+  if (lane == 0) rowf[n] = pow2_to(mx, 10);
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void unpack8(const uint4 &w, float (&v)[8]) {
+  const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kBf16) {
+      v[2 * i] = __uint_as_float(a[i] << 16);
+      v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&a[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Blocks 0..M-1: x' = fp16(x s e) of one token, in the order the dequantization yields
+// (0, 4, 1, 5, 2, 6, 3, 7 of every 8 channels), and (e, 1 / e).  The blocks behind them:
+// the row factors, one warp per packed row.  A token is read once: each thread keeps up
+// to 4 vectors (K <= 8192 at 256 threads) between the maximum and the conversion; deeper
+// layers read the rest again, from L1 or L2.
+constexpr int kStageThreads = 256;
+constexpr int kStageKeep = 4;
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kStageThreads)
+    fused_stage_x(const uint16_t *X, const float *awq_s, int64_t M, int64_t K, const uint16_t *scales, int64_t kg,
+                  int64_t N, uint16_t *xp, float2 *tokf, float2 *rowf) {
+  grid_launch_dependents();
+  if (blockIdx.x >= M) {
+    const int64_t n = ((int64_t)blockIdx.x - M) * (kStageThreads / 32) + (threadIdx.x >> 5);
+    if (n < N) row_factor(scales, kg, n, rowf);
+    return;
+  }
+  __shared__ float red[kStageThreads / 32];
+  const int64_t m = blockIdx.x, nv = K / 8;
+  const uint4 *row = reinterpret_cast<const uint4 *>(X + m * K);
+  auto scaled = [&](const uint4 &w, int64_t v, float (&f)[8]) {
+    unpack8<kBf16>(w, f);
+    if (awq_s) {
+      const float4 a = reinterpret_cast<const float4 *>(awq_s)[2 * v], b = reinterpret_cast<const float4 *>(awq_s)[2 * v + 1];
+      f[0] *= a.x; f[1] *= a.y; f[2] *= a.z; f[3] *= a.w;
+      f[4] *= b.x; f[5] *= b.y; f[6] *= b.z; f[7] *= b.w;
+    }
+  };
+  uint4 keep[kStageKeep];
+  float mx = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kStageKeep; ++i) {
+    const int64_t v = threadIdx.x + (int64_t)i * kStageThreads;
+    keep[i] = v < nv ? row[v] : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < kStageKeep; ++i) {
+    const int64_t v = threadIdx.x + (int64_t)i * kStageThreads;
+    if (v >= nv) break;
+    float f[8];
+    scaled(keep[i], v, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(f[j]));
+  }
+  for (int64_t v = threadIdx.x + (int64_t)kStageKeep * kStageThreads; v < nv; v += kStageThreads) {
+    float f[8];
+    scaled(row[v], v, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(f[j]));
+  }
+  const float2 e = pow2_to(block_max(mx, red), 13);
+  if (threadIdx.x == 0) tokf[m] = e;
+  uint4 *out = reinterpret_cast<uint4 *>(xp + m * K);
+  auto put = [&](const uint4 &w, int64_t v) {
+    float f[8];
+    scaled(w, v, f);
+    out[v] = make_uint4(half2_bits(f[0] * e.x, f[4] * e.x), half2_bits(f[1] * e.x, f[5] * e.x),
+                        half2_bits(f[2] * e.x, f[6] * e.x), half2_bits(f[3] * e.x, f[7] * e.x));
+  };
+#pragma unroll
+  for (int i = 0; i < kStageKeep; ++i) {
+    const int64_t v = threadIdx.x + (int64_t)i * kStageThreads;
+    if (v < nv) put(keep[i], v);
+  }
+  for (int64_t v = threadIdx.x + (int64_t)kStageKeep * kStageThreads; v < nv; v += kStageThreads) put(row[v], v);
+}
+
+__global__ void __launch_bounds__(kStageThreads)
+    fused_row_factors(const uint16_t *scales, int64_t kg, int64_t N, float2 *rowf) {
+  grid_launch_dependents();
+  const int64_t n = (int64_t)blockIdx.x * (kStageThreads / 32) + (threadIdx.x >> 5);
+  if (n < N) row_factor(scales, kg, n, rowf);
+}
+
+// dZ of `kVec` consecutive rows n.. of token m (gated: n.. lies on one side of F).
+template <bool kGated, int kVec>
+__device__ __forceinline__ void dz_at(const void *dY, const void *Z, int dtype, int act, int64_t N, int64_t m, int64_t n,
+                                      float (&d)[kVec]) {
+  const int64_t F = kGated ? N / 2 : N, f = kGated && n >= F ? n - F : n;
+  float g[kVec], a[kVec], u[kVec];
+  auto get = [&](const void *p, int64_t i, float (&v)[kVec]) {
+    if constexpr (kVec == 8) {
+      const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
+      if (dtype == 2) unpack8<true>(w, v);
+      else unpack8<false>(w, v);
+    } else {
+      v[0] = load_as_float(p, dtype, i);
+    }
+  };
+  get(dY, m * F + f, g);
+  if (Z) get(Z, m * N + f, a);
+  if (kGated && n < F) get(Z, m * N + F + f, u);
+#pragma unroll
+  for (int j = 0; j < kVec; ++j) {
+    float y = 0.0f, s = 1.0f;
+    if (Z) act_both(a[j], act, y, s);
+    d[j] = !kGated ? g[j] * s : n < F ? g[j] * u[j] * s : g[j] * y;
+  }
+}
+
+// dz' = fp16(dZ / r[n] * e) of one token per block, natural order, columns N.. up to the
+// row stride `ld` zero, and (e, 1 / e).  Two passes: the second finds its inputs in L2.
+template <bool kGated, int kVec>
+__global__ void __launch_bounds__(512)
+    fused_stage_dz(const void *dY, const void *Z, int dtype, int act, int64_t N, int64_t ld, const float2 *rowf,
+                   uint16_t *dzp, float2 *tokf) {
+  grid_launch_dependents();
+  grid_dependency_wait();  // the row factors
+  __shared__ float red[16];
+  const int64_t m = blockIdx.x;
+  float mx = 0.0f;
+  for (int64_t n = (int64_t)threadIdx.x * kVec; n < N; n += 512 * kVec) {
+    float d[kVec];
+    dz_at<kGated, kVec>(dY, Z, dtype, act, N, m, n, d);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) mx = fmaxf(mx, fabsf(d[j] * rowf[n + j].y));
+  }
+  const float2 e = pow2_to(block_max(mx, red), 13);
+  if (threadIdx.x == 0) tokf[m] = e;
+  for (int64_t n = (int64_t)threadIdx.x * kVec; n < ld; n += 512 * kVec) {
+    float d[kVec] = {};
+    if (n < N) {
+      dz_at<kGated, kVec>(dY, Z, dtype, act, N, m, n, d);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) d[j] = d[j] * rowf[n + j].y * e.x;
+    }
+    if constexpr (kVec == 8)
+      *reinterpret_cast<uint4 *>(dzp + m * ld + n) = make_uint4(half2_bits(d[0], d[1]), half2_bits(d[2], d[3]),
+                                                                half2_bits(d[4], d[5]), half2_bits(d[6], d[7]));
+    else
+      dzp[m * ld + n] = __half_as_ushort(__float2half_rn(d[0]));
+  }
+}
+
+// dbias: sums of dZ over the tokens.  A block takes 32 * kVec columns and a range of
+// tokens, 8 tokens at a time (one per warp); the ranges' sums go to part [ranges][N] and
+// a second kernel adds them in order, so the result does not depend on timing.
+template <bool kGated, int kVec>
+__global__ void __launch_bounds__(256)
+    fused_dbias_part(const void *dY, const void *Z, int dtype, int act, int64_t M, int64_t N, int64_t per, float *part) {
+  __shared__ float sum[8][32 * kVec];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t n = ((int64_t)blockIdx.x * 32 + lane) * kVec;
+  const int64_t m1 = min(M, ((int64_t)blockIdx.y + 1) * per);
+  float acc[kVec] = {};
+  if (n < N)
+    for (int64_t m = (int64_t)blockIdx.y * per + w; m < m1; m += 8) {
+      float d[kVec];
+      dz_at<kGated, kVec>(dY, Z, dtype, act, N, m, n, d);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) acc[j] += d[j];
+    }
+#pragma unroll
+  for (int j = 0; j < kVec; ++j) sum[w][lane * kVec + j] = acc[j];
+  __syncthreads();
+  for (int c = threadIdx.x; c < 32 * kVec; c += 256) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += sum[i][c];
+    const int64_t col = (int64_t)blockIdx.x * 32 * kVec + c;
+    if (col < N) part[blockIdx.y * N + col] = s;
+  }
+}
+
+__global__ void __launch_bounds__(256) fused_dbias_sum(const float *part, int ranges, int64_t N, float *dbias) {
+  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (n >= N) return;
+  float s = 0.0f;
+  for (int i = 0; i < ranges; ++i) s += part[i * N + n];
+  dbias[n] = s;
+}
+
+// ------------------------------------------------------------------ launches
+template <typename... Args>
+cudaError_t launch_pdl(void (*kern)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                       typename std::common_type<Args>::type... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+cudaError_t launch_fused_stage_x(const void *X, bool bf16, const float *awq_s, int64_t M, int64_t K,
+                                 const uint16_t *scales, int64_t kg, int64_t N, uint16_t *xp, float2 *tokf, float2 *rowf,
+                                 cudaStream_t s) {
+  const unsigned grid = (unsigned)(M + (N + kStageThreads / 32 - 1) / (kStageThreads / 32));
+  const uint16_t *x = static_cast<const uint16_t *>(X);
+  if (bf16) fused_stage_x<true><<<grid, kStageThreads, 0, s>>>(x, awq_s, M, K, scales, kg, N, xp, tokf, rowf);
+  else fused_stage_x<false><<<grid, kStageThreads, 0, s>>>(x, awq_s, M, K, scales, kg, N, xp, tokf, rowf);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_fused_stage_dz(const void *dY, const void *Z, int dtype, int act, bool gated, int64_t M, int64_t N,
+                                  int64_t ld, const uint16_t *scales, int64_t kg, uint16_t *dzp, float2 *tokf,
+                                  float2 *rowf, cudaStream_t s) {
+  fused_row_factors<<<(unsigned)((N + kStageThreads / 32 - 1) / (kStageThreads / 32)), kStageThreads, 0, s>>>(
+      scales, kg, N, rowf);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // 16-byte vectors where every row (and its gated half) starts on one
+  const bool vec = (gated ? N / 2 : N) % 8 == 0;
+  auto k = gated ? (vec ? fused_stage_dz<true, 8> : fused_stage_dz<true, 1>)
+                 : (vec ? fused_stage_dz<false, 8> : fused_stage_dz<false, 1>);
+  return launch_pdl(k, dim3((unsigned)M), dim3(512), 0, s, dY, Z, dtype, act, N, ld, (const float2 *)rowf, dzp, tokf);
+}
+
+// Token ranges of dbias: about four blocks per SM, at least 8 tokens each.
+int64_t fused_dbias_ranges(int64_t M, int64_t N, bool vec) {
+  const int64_t cols = (N + (vec ? 256 : 32) - 1) / (vec ? 256 : 32);
+  int64_t r = (600 + cols - 1) / cols;
+  r = r > (M + 7) / 8 ? (M + 7) / 8 : r;
+  return r < 1 ? 1 : r;
+}
+
+cudaError_t launch_fused_dbias(const void *dY, const void *Z, int dtype, int act, bool gated, int64_t M, int64_t N,
+                               float *part, float *dbias, cudaStream_t s) {
+  const bool vec = (gated ? N / 2 : N) % 8 == 0;
+  int64_t ranges = fused_dbias_ranges(M, N, vec);
+  const int64_t per = (M + ranges - 1) / ranges;
+  ranges = (M + per - 1) / per;
+  const dim3 grid((unsigned)((N + (vec ? 256 : 32) - 1) / (vec ? 256 : 32)), (unsigned)ranges);
+  float *to = ranges == 1 ? dbias : part;
+  auto k = gated ? (vec ? fused_dbias_part<true, 8> : fused_dbias_part<true, 1>)
+                 : (vec ? fused_dbias_part<false, 8> : fused_dbias_part<false, 1>);
+  k<<<grid, 256, 0, s>>>(dY, Z, dtype, act, M, N, per, to);
+  if (ranges > 1) fused_dbias_sum<<<(unsigned)((N + 255) / 256), 256, 0, s>>>(part, (int)ranges, N, dbias);
+  return cudaGetLastError();
+}
+
+}  // namespace w4

@@ -1,0 +1,730 @@
+// fused_tc.cu -- the fused operators' products on the 5th-generation tensor cores.
+//
+//   kLinear, kGated   D[n][m] = sum_k W^[n][k] x'[m][k]     (Z = X . W^T)
+//   kGrad             D[k][m] = sum_n W^[n][k] dz'[m][n]    (dX = dZ . W^)
+//
+// One persistent CTA per SM computes tiles of 128 rows x BN tokens.  A gated tile is 64
+// gate rows and the 64 up rows that belong to them, so that act(G) * U is formed in the
+// tile's epilogue and neither G nor U goes to memory (unless they are asked for).
+//
+// Roles (512 threads): warp 0 loads activations (TMA), warp 1 loads codes (TMA), warp 2
+// issues the MMAs, warp 3 owns TMEM, warps 4..7 write results, warps 8..15 dequantize in
+// two sets of four that take turns.  The MMA and TMA instructions sit under elect.sync in
+// warp-uniform code: issued from a thread-dependent branch, each one costs the issuing
+// thread about 78 ns for operands moved to uniform registers one by one, whatever its
+// size (measured; 4 x 128x256x16 in 313 ns instead of 280).
+//
+// Forward, the dequantized weights are the MMA's A operand in tensor memory: a thread
+// owns a row, its TMEM lane.  For the gradient the contraction runs over the rows, and
+// A needs W^ transposed: the threads write W^ as it lies (channels contiguous) into
+// shared memory, which the MMA reads as an MN-major operand.  Both ways a word of eight
+// codes takes 13 instructions: four pairs of exact 1024 + q (or 1024 + 16 q) by LOP3, an
+// exact subtraction giving q - z, and one product with the scaled group scale, which is
+// the only rounding (fp16, 2^-11).  bf16 operands would round to 2^-8: on top of a bf16
+// output's own rounding that was half as much error again.
+//
+// Two accumulators in TMEM alternate between tiles, so a tile's epilogue runs under the
+// next one's products; with BN <= 208 they leave room for three 64-deep A buffers.
+//
+// Scheduling: whole waves of tiles first, then the tiles that are left are cut along the
+// contraction into one contiguous range per CTA; the pieces' fp32 partials are summed, in
+// order, by fused_finish, which also runs the epilogue.  No block waits for another.
+#include "act.cuh"
+#include "common.cuh"
+
+namespace w4 {
+
+enum FusedMode { kLinear = 0, kGated = 1, kGrad = 2 };
+
+struct FusedEpi {
+  int64_t M, N;             // tokens, output columns of a linear / gradient call, F of a gated one
+  const float2 *rowf;       // forward: (r, 1 / r) per packed row
+  const float2 *tokf;       // (e, 1 / e) per token
+  const float *bias;        // forward, or NULL
+  const float *colmul;      // gradient: awq_s, or NULL
+  const void *residual;     // or NULL
+  void *Z, *Y;              // Z or NULL
+  int act, z_dtype, y_dtype, vec;  // vec: 8 outputs in a row start on 16 bytes
+};
+
+struct FusedTcParams {
+  FusedEpi epi;
+  const uint16_t *scales, *zeros;
+  int64_t rows;             // packed rows
+  int64_t kg;               // groups per packed row
+  int gshift;               // log2(group)
+  int bn, mt, rt, units;    // token tile, token tiles, row tiles, 128-deep units per tile
+  int gt;                   // token tiles per raster block
+  int full;                 // tiles computed whole
+  int tiles, tail_ctas;     // all tiles; CTAs that share the rest
+  float *part;              // [2 * tail_ctas][bn][128] partial tiles
+};
+
+namespace ftc {
+
+constexpr int kThreads = 512;
+constexpr int kCodeStages = 4, kCodeStage = 128 * 64;
+constexpr int kAct = 64 * 2;             // bytes of a token's 64 channels in a stage
+constexpr int kStageOut = 32 * 128 * 4;  // 32 tokens of a tile in fp32
+constexpr int kGradA = 3, kGradAStage = 64 * 128 * 2;
+constexpr int kMaxBn = 208;
+constexpr int kMaxActStages = 8;
+
+__host__ __device__ constexpr int fixed_bytes(bool grad) {
+  return 1024 + kCodeStages * kCodeStage + 2 * kStageOut + (grad ? kGradA * kGradAStage : 0) + 2 * 256 * 4 + 512;
+}
+__host__ __device__ inline int act_stages(int bn, bool grad) {
+  const int n = (227 * 1024 - fixed_bytes(grad)) / (bn * kAct);
+  return n > kMaxActStages ? kMaxActStages : n;
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T
+__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// mbar_wait by a whole warp with one answer, so that the warp-wide instructions behind it
+// are reached by all lanes or by none.
+__device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, int err_bit) {
+  return __all_sync(~0u, mbar_wait(bar, parity, err_bit));
+}
+
+// AND over the four epilogue warps (named barrier 1): either all of them go on or none.
+__device__ __forceinline__ bool vote_epilogue(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void bar_epilogue() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b),
+                            *reinterpret_cast<const __half2 *>(&c));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t dup_half(float v) {
+  const __half2 h = __float2half2_rn(v);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// A group's constants as fp16 pairs: scale * r, 1024 + z, -(64 + z).
+struct GroupK {
+  uint32_t s, zlo, zhi;
+  __device__ __forceinline__ void set(uint16_t scale, uint16_t zero, float r) {
+    const float z = half_bits_to_float(zero);
+    s = dup_half(half_bits_to_float(scale) * r);
+    zlo = dup_half(1024.0f + z);
+    zhi = dup_half(-64.0f - z);
+  }
+};
+
+// Eight codes -> pairs (0,4) (1,5) (2,6) (3,7) of fp16 (q - z) * scale * r.  1024 + q and
+// 64 + q are exact in fp16, so are their differences; the product is rounded once.
+__device__ __forceinline__ void dequant8(uint32_t w, const GroupK &g, uint32_t (&o)[4]) {
+  const uint32_t w8 = w >> 8;
+  const uint32_t a = lop3_and_or(w, 0x000F000Fu, 0x64006400u), b = lop3_and_or(w, 0x00F000F0u, 0x64006400u);
+  const uint32_t c = lop3_and_or(w8, 0x000F000Fu, 0x64006400u), d = lop3_and_or(w8, 0x00F000F0u, 0x64006400u);
+  constexpr uint32_t k16th = 0x2C002C00u;  // 1/16
+  o[0] = hmul2(hsub2(a, g.zlo), g.s);
+  o[1] = hmul2(hfma2(b, k16th, g.zhi), g.s);
+  o[2] = hmul2(hsub2(c, g.zlo), g.s);
+  o[3] = hmul2(hfma2(d, k16th, g.zhi), g.s);
+}
+
+// One CTA's share of the work: tiles blockIdx, blockIdx + grid, ... below `full`, then its
+// range of the remaining tiles' units.  slot < 0: a whole tile.
+struct Work {
+  const FusedTcParams &p;
+  int t;
+  int64_t u, u1, base;
+  int nth;
+  __device__ __forceinline__ explicit Work(const FusedTcParams &q) : p(q), t(blockIdx.x), u(0), u1(0), nth(0) {
+    if ((int)blockIdx.x < p.tail_ctas) {
+      const int64_t total = (int64_t)(p.tiles - p.full) * p.units;
+      u = total * blockIdx.x / p.tail_ctas;
+      u1 = total * (blockIdx.x + 1) / p.tail_ctas;
+    }
+  }
+  __device__ __forceinline__ bool next(int &tile, int &k0, int &k1, int &slot) {
+    if (t < p.full) {
+      tile = t;
+      k0 = 0;
+      k1 = p.units;
+      slot = -1;
+      t += gridDim.x;
+      return true;
+    }
+    if (u >= u1) return false;
+    const int i = (int)(u / p.units);
+    tile = p.full + i;
+    k0 = (int)(u - (int64_t)i * p.units);
+    k1 = (int)min((int64_t)p.units, k0 + (u1 - u));
+    u += k1 - k0;
+    slot = k1 - k0 == p.units ? -1 : 2 * (int)blockIdx.x + nth;
+    ++nth;
+    return true;
+  }
+};
+
+// Raster: blocks of gt token tiles, inside a block the token tiles of one row tile side
+// by side, so that the CTAs at work at one time share activations and weights in L2.
+__device__ __forceinline__ void tile_at(const FusedTcParams &p, int t, int &row, int &tok) {
+  const int per = p.gt * p.rt, g = t / per, r = t - g * per;
+  const int w = min(p.gt, p.mt - g * p.gt);
+  row = r / w;
+  tok = g * p.gt + r - row * w;
+}
+
+// The k that tile row r of a gradient tile holds: the dequantization's pairs put code
+// {0,4,1,5,2,6,3,7}[j] of a word at place j.
+__device__ __forceinline__ int grad_row(int r) { return (r & ~7) | ((r & 1) << 2) | ((r >> 1) & 3); }
+
+__device__ __forceinline__ void put8(void *p, int dtype, int64_t i, const float (&v)[8]) {
+  if (dtype == 0) {
+    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
+    o[0] = make_float4(v[0], v[1], v[2], v[3]);
+    o[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else if (dtype == 1) {
+    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) =
+        make_uint4(half2_bits(v[0], v[1]), half2_bits(v[2], v[3]), half2_bits(v[4], v[5]), half2_bits(v[6], v[7]));
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+      w[j] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+__device__ __forceinline__ void add8(const void *p, int dtype, int64_t i, float (&v)[8]) {
+  float a[8];
+  if (dtype == 0) {
+    const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+    const float4 x = q[0], y = q[1];
+    a[0] = x.x; a[1] = x.y; a[2] = x.z; a[3] = x.w; a[4] = y.x; a[5] = y.y; a[6] = y.z; a[7] = y.w;
+  } else {
+    const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
+    if (dtype == 2) unpack8<true>(w, a);
+    else unpack8<false>(w, a);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] += a[j];
+}
+
+// Stores v[0..8) at columns n.. of a row that starts at element `row`; n + j < lim.
+__device__ __forceinline__ void put_row(void *p, int dtype, int64_t row, int64_t n, int64_t lim, bool vec,
+                                        const float (&v)[8]) {
+  if (vec && n + 8 <= lim) {
+    put8(p, dtype, row + n, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (n + j < lim) store_from_float(p, dtype, row + n + j, v[j]);
+  }
+}
+
+// Factor and bias of eight output columns (0 behind the last).
+struct ColK {
+  float f[8], b[8];
+  // first: packed row (forward) or channel (gradient) of column 0
+  __device__ __forceinline__ void load(const FusedEpi &e, bool grad, int64_t first, int64_t n, int64_t lim) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool ok = n + j < lim;
+      f[j] = !ok ? 0.0f : grad ? (e.colmul ? e.colmul[first + j] : 1.0f) : e.rowf[first + j].y;
+      b[j] = ok && e.bias ? e.bias[first + j] : 0.0f;
+    }
+  }
+};
+
+// z = v * factor / e + bias
+__device__ __forceinline__ void scale8(const float (&v)[8], const ColK &c, float inv, float (&z)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) z[j] = v[j] * c.f[j] * inv + c.b[j];
+}
+
+__device__ __forceinline__ void finish_linear(const FusedEpi &e, int64_t m, int64_t n, float (&z)[8]) {
+  const int64_t row = m * e.N;
+  if (e.Z) put_row(e.Z, e.z_dtype, row, n, e.N, e.vec, z);
+  if (e.act != kActNone) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] = act_fwd(z[j], e.act);
+  }
+  if (e.residual) {
+    if (e.vec && n + 8 <= e.N) {
+      add8(e.residual, e.y_dtype, row + n, z);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (n + j < e.N) z[j] += load_as_float(e.residual, e.y_dtype, row + n + j);
+    }
+  }
+  put_row(e.Y, e.y_dtype, row, n, e.N, e.vec, z);
+}
+
+__device__ __forceinline__ void finish_gated(const FusedEpi &e, int64_t m, int64_t f, float (&g)[8], const float (&u)[8]) {
+  if (e.Z) {
+    put_row(e.Z, e.z_dtype, m * 2 * e.N, f, e.N, e.vec, g);
+    put_row(e.Z, e.z_dtype, m * 2 * e.N + e.N, f, e.N, e.vec, u);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) g[j] = act_fwd(g[j], e.act) * u[j];
+  put_row(e.Y, e.y_dtype, m * e.N, f, e.N, e.vec, g);
+}
+
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+}  // namespace ftc
+
+template <int kMode>
+__global__ void __launch_bounds__(ftc::kThreads, 1)
+    fused_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmP,
+                    const FusedTcParams p) {
+  using namespace ftc;
+  constexpr bool kIsGrad = kMode == kGrad;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int ns = act_stages(p.bn, kIsGrad);
+  const int act_stage = p.bn * kAct;
+  uint8_t *sC = smem;
+  float *sOut = reinterpret_cast<float *>(sC + kCodeStages * kCodeStage);
+  uint8_t *sA = reinterpret_cast<uint8_t *>(sOut) + 2 * kStageOut;
+  uint8_t *sX = sA + (kIsGrad ? kGradA * kGradAStage : 0);
+  float *sTok = reinterpret_cast<float *>(sX + ns * act_stage);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sTok + 256);
+  uint64_t *xfull = bars, *xempty = xfull + kMaxActStages;
+  uint64_t *cfull = xempty + kMaxActStages, *cempty = cfull + kCodeStages;
+  uint64_t *afull = cempty + kCodeStages, *aempty = afull + 8;
+  uint64_t *dfull = aempty + 8, *dempty = dfull + 2;
+  uint32_t *holder = reinterpret_cast<uint32_t *>(dempty + 2);
+
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
+  const int lane = threadIdx.x & 31;
+  // A buffers: TMEM columns behind the two accumulators, or shared memory
+  const int na = kIsGrad ? kGradA : min(8, (512 - 2 * p.bn) / 32);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ns; ++i) {
+      mbar_init(&xfull[i], 1);
+      mbar_init(&xempty[i], 1);
+    }
+    for (int i = 0; i < kCodeStages; ++i) {
+      mbar_init(&cfull[i], 1);
+      mbar_init(&cempty[i], 128);
+    }
+    for (int i = 0; i < na; ++i) {
+      mbar_init(&afull[i], 128);
+      mbar_init(&aempty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&dfull[i], 1);
+      mbar_init(&dempty[i], 128);
+    }
+    fence_barrier_init();
+    prefetch_tensormap(&tmX);
+    prefetch_tensormap(&tmP);
+  }
+  if (warp == 3) {
+    tmem_alloc(holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *holder;
+  bool ok = true;
+
+  Work work(p);
+  int tile, k0, k1, slot;
+  if (warp == 0) {
+    // ---- activations: one box of BN tokens x 64 per stage
+    grid_dependency_wait();
+    int s = 0;
+    uint32_t ph = 0;
+    while (ok && work.next(tile, k0, k1, slot)) {
+      int row, tok;
+      tile_at(p, tile, row, tok);
+      for (int b = 2 * k0; b < 2 * k1; ++b) {
+        if (!wait_all(&xempty[s], ph ^ 1u, kErrTimeoutTma)) { ok = false; break; }
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&xfull[s], (uint32_t)act_stage);
+          tma_load_2d(sX + s * act_stage, &tmX, &xfull[s], b * 64, tok * p.bn);
+        }
+        __syncwarp();
+        if (++s == ns) s = 0, ph ^= 1u;
+      }
+    }
+  } else if (warp == 1) {
+    // ---- codes: 128 rows x 128 channels per stage (64-byte rows, 64-byte swizzle)
+    int s = 0;
+    uint32_t ph = 0;
+    while (ok && work.next(tile, k0, k1, slot)) {
+      int row, tok;
+      tile_at(p, tile, row, tok);
+      for (int u = k0; u < k1; ++u) {
+        if (!wait_all(&cempty[s], ph ^ 1u, kErrTimeoutTma)) { ok = false; break; }
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&cfull[s], kCodeStage);
+          uint8_t *dst = sC + s * kCodeStage;
+          if (kMode == kGrad) {
+            tma_load_2d(dst, &tmP, &cfull[s], row * 64, u * 128);
+          } else if (kMode == kLinear) {
+            tma_load_2d(dst, &tmP, &cfull[s], u * 64, row * 128);
+          } else {
+            tma_load_2d(dst, &tmP, &cfull[s], u * 64, row * 64);
+            tma_load_2d(dst + kCodeStage / 2, &tmP, &cfull[s], u * 64, (int)p.epi.N + row * 64);
+          }
+        }
+        __syncwarp();
+        if (++s == kCodeStages) s = 0, ph ^= 1u;
+      }
+    }
+  } else if (warp == 2) {
+    // ---- products
+    const uint32_t idesc = idesc_f16(false, p.bn) | (kIsGrad ? 1u << 15 : 0u);  // bit 15: A is MN-major
+    int s = 0, a = 0, d = 0;
+    uint32_t xph = 0, aph = 0, dph = 0;
+    while (ok && work.next(tile, k0, k1, slot)) {
+      if (!wait_all(&dempty[d], dph ^ 1u, kErrTimeoutMma)) { ok = false; break; }
+      tc_fence_after();
+      const uint32_t acc = tmem + (uint32_t)(d * p.bn);
+      for (int b = 2 * k0; b < 2 * k1; ++b) {
+        if (!wait_all(&xfull[s], xph, kErrTimeoutMma) || !wait_all(&afull[a], aph, kErrTimeoutMma)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t bd = smem_desc_k_sw128(smem_u32(sX + s * act_stage));
+        const bool first = b == 2 * k0;
+        if (elect_one()) {
+          if constexpr (kIsGrad) {
+            // MN-major A: 64-channel halves 8192 bytes apart (leading offset), 8-row
+            // groups of the contraction 1024 bytes apart (stride offset)
+            const uint64_t ad = (smem_desc_k_sw128(smem_u32(sA + a * kGradAStage)) & ~((uint64_t)0x3FFF << 16)) |
+                                ((uint64_t)(8192 >> 4) << 16);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              tc_mma_ss(acc, ad + (uint64_t)(128 * j), bd + (uint64_t)(2 * j), idesc, first && j == 0 ? 0u : 1u);
+          } else {
+            const uint32_t at = tmem + (uint32_t)(2 * p.bn + 32 * a);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              tc_mma_ts(acc, at + 8 * j, bd + (uint64_t)(2 * j), idesc, first && j == 0 ? 0u : 1u);
+          }
+          tc_commit(&xempty[s]);
+          tc_commit(&aempty[a]);
+          if (b == 2 * k1 - 1) tc_commit(&dfull[d]);
+        }
+        __syncwarp();
+        if (++s == ns) s = 0, xph ^= 1u;
+        if (++a == na) a = 0, aph ^= 1u;
+      }
+      d ^= 1;
+      if (d == 0) dph ^= 1u;
+    }
+  } else if (warp >= 8) {
+    // ---- dequantization: set (warp - 8) / 4 takes every other unit
+    const int set = (warp - 8) >> 2, wq = warp & 3;
+    grid_dependency_wait();  // the row factors
+    int i = 0;               // units seen by both sets
+    while (ok && work.next(tile, k0, k1, slot)) {
+      int row, tok;
+      tile_at(p, tile, row, tok);
+      // forward: this thread's packed row, TMEM lane 32 wq + lane; its group constants are
+      // fetched one unit ahead (of this set's)
+      const int r = 32 * wq + lane;
+      int64_t n = 0;
+      bool row_ok = true;
+      float rf = 0.0f;
+      if constexpr (!kIsGrad) {
+        if (kMode == kLinear) {
+          n = (int64_t)row * 128 + r;
+          row_ok = n < p.rows;
+        } else {
+          const int64_t f = (int64_t)row * 64 + (r & 63);
+          n = r < 64 ? f : p.epi.N + f;
+          row_ok = f < p.epi.N;
+        }
+        rf = row_ok ? p.epi.rowf[n].x : 0.0f;
+      }
+      // gradient: rows n of the contraction, two per unit (blocks of 64), channel half kh
+      const int nl = 32 * (wq & 1) + lane, kh = wq >> 1;
+      uint16_t sc[4], zc[4];  // forward: 32-channel pieces of a unit; gradient: [block][32-channel piece]
+      float rfs[2] = {0.0f, 0.0f};
+      auto fetch = [&](int u) {
+        if constexpr (kIsGrad) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int64_t nn = (int64_t)u * 128 + h * 64 + nl;
+            const bool in = nn < p.rows;
+            rfs[h] = in ? p.epi.rowf[nn].x : 0.0f;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int64_t g = ((int64_t)row * 128 + kh * 64 + c * 32) >> p.gshift;
+              const bool gin = in && g < p.kg;
+              sc[2 * h + c] = gin ? __ldg(p.scales + nn * p.kg + g) : (uint16_t)0;
+              zc[2 * h + c] = gin ? __ldg(p.zeros + nn * p.kg + g) : (uint16_t)0;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (c > 0 && p.gshift == 7) {
+              sc[c] = sc[0];
+              zc[c] = zc[0];
+              continue;
+            }
+            const int64_t g = ((int64_t)u * 128 + c * 32) >> p.gshift;
+            const bool in = row_ok && g < p.kg;
+            sc[c] = in ? __ldg(p.scales + n * p.kg + g) : (uint16_t)0;
+            zc[c] = in ? __ldg(p.zeros + n * p.kg + g) : (uint16_t)0;
+          }
+        }
+      };
+      const int first = k0 + ((i + set) & 1);  // this set's first unit of the range
+      if (first < k1) fetch(first);
+      for (int u = first; u < k1; u += 2) {
+        const int iu = i + (u - k0);
+        const int s = iu % kCodeStages;
+        GroupK g[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) g[c].set(sc[c], zc[c], kIsGrad ? rfs[c >> 1] : rf);
+        if (u + 2 < k1) fetch(u + 2);
+        if (!wait_all(&cfull[s], (uint32_t)(iu / kCodeStages) & 1u, kErrTimeoutDequant)) { ok = false; break; }
+        const uint32_t src = smem_u32(sC + s * kCodeStage);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int ia = 2 * iu + h, a = ia % na;
+          // forward: row r, chunks 2h, 2h + 1;  gradient: row 64 h + nl, chunks 2 kh, 2 kh + 1
+          const int cr = kIsGrad ? 64 * h + nl : r, cc = kIsGrad ? 2 * kh : 2 * h;
+          const uint32_t base = src + (uint32_t)(cr * 64), sw = (uint32_t)((cr >> 1) & 3);
+          const uint4 q0 = lds128(base + ((((uint32_t)cc) ^ sw) << 4));
+          const uint4 q1 = lds128(base + ((((uint32_t)cc + 1u) ^ sw) << 4));
+          const uint32_t wd[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+          uint32_t out[32];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint32_t o[4];
+            // constants: forward piece 2h + (j / 4) of the unit, gradient [h][j / 4]
+            dequant8(wd[j], g[2 * h + (j >> 2)], o);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) out[4 * j + x] = o[x];
+          }
+          if (!wait_all(&aempty[a], ((uint32_t)(ia / na) & 1u) ^ 1u, kErrTimeoutDequant)) { ok = false; break; }
+          if constexpr (kIsGrad) {
+            const uint32_t dst = smem_u32(sA + a * kGradAStage) + (uint32_t)(kh * 8192 + nl * 128);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (uint32_t)((j ^ (nl & 7)) << 4)),
+                           "r"(out[4 * j]), "r"(out[4 * j + 1]), "r"(out[4 * j + 2]), "r"(out[4 * j + 3])
+                           : "memory");
+            fence_proxy_async_smem();
+          } else {
+            tc_fence_after();
+            tmem_st_32x32b_x32(tmem + ((uint32_t)(32 * wq) << 16) + (uint32_t)(2 * p.bn + 32 * a), out);
+            tc_wait_st();
+            tc_fence_before();
+          }
+          mbar_arrive(&afull[a]);
+        }
+        if (!ok) break;
+        // The codes are given back only here, behind the stores that needed them: an arrive
+        // right behind the loads let the loads sink below it, and now and then read the
+        // stage's next contents.
+        mbar_arrive(&cempty[s]);
+      }
+      i += k1 - k0;
+    }
+  } else if (warp >= 4) {
+    // ---- epilogue
+    const int q = warp & 3, tid = threadIdx.x - 128;
+    grid_dependency_wait();  // row and token factors
+    const FusedEpi &e = p.epi;
+    int d = 0;
+    uint32_t dph = 0;
+    while (work.next(tile, k0, k1, slot)) {
+      int row, tok;
+      tile_at(p, tile, row, tok);
+      const int64_t m0 = (int64_t)tok * p.bn;
+      for (int t = tid; t < p.bn; t += 128) sTok[t] = m0 + t < e.M ? e.tokf[m0 + t].y : 0.0f;
+      ColK c0, c1;
+      const int64_t n = kMode == kGated ? (int64_t)row * 64 + 8 * (tid & 7) : (int64_t)row * 128 + 8 * (tid & 15);
+      if (slot < 0) {
+        c0.load(e, kIsGrad, n, n, e.N);
+        if (kMode == kGated) c1.load(e, false, e.N + n, n, e.N);
+      }
+      if (!vote_epilogue(mbar_wait(&dfull[d], dph, kErrTimeoutEpilogue))) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(d * p.bn);
+      const int prow = kIsGrad ? grad_row(32 * q + lane) : 32 * q + lane;
+      for (int c = 0; c * 32 < p.bn; ++c) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(acc + (uint32_t)(c * 32), v);
+        tc_wait_ld();
+        if ((c + 1) * 32 >= p.bn) {
+          tc_fence_before();
+          mbar_arrive(&dempty[d]);
+        }
+        float *st = sOut + (c & 1) * (kStageOut / 4);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) st[j * 128 + prow] = __uint_as_float(v[j]);
+        bar_epilogue();
+        const int lim = (int)min((int64_t)p.bn, e.M - m0) - c * 32;  // valid tokens from this chunk on
+        if (slot >= 0) {
+          float *dst = p.part + ((int64_t)slot * p.bn + c * 32) * 128;
+#pragma unroll
+          for (int s = 0; s < 8; ++s) {
+            const int t = s * 4 + (tid >> 5);
+            if (t < lim)
+              reinterpret_cast<float4 *>(dst + t * 128)[tid & 31] = reinterpret_cast<const float4 *>(st + t * 128)[tid & 31];
+          }
+        } else if (kMode == kGated) {
+          if (n < e.N)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              const int t = s * 16 + (tid >> 3);
+              if (t < lim) {
+                float x[8], g[8], u[8];
+                const float inv = sTok[c * 32 + t];
+                load8(st + t * 128 + 8 * (tid & 7), x);
+                scale8(x, c0, inv, g);
+                load8(st + t * 128 + 64 + 8 * (tid & 7), x);
+                scale8(x, c1, inv, u);
+                finish_gated(e, m0 + c * 32 + t, n, g, u);
+              }
+            }
+        } else {
+          if (n < e.N)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              const int t = s * 8 + (tid >> 4);
+              if (t < lim) {
+                float x[8], z[8];
+                load8(st + t * 128 + 8 * (tid & 15), x);
+                scale8(x, c0, sTok[c * 32 + t], z);
+                finish_linear(e, m0 + c * 32 + t, n, z);
+              }
+            }
+        }
+      }
+      d ^= 1;
+      if (d == 0) dph ^= 1u;
+      bar_epilogue();  // sTok is read until here
+    }
+  }
+  // A wait that ran out: copies of this CTA may still be in flight; give them time to land.
+  if (!ok) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) {}
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 3) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Sums the partial tiles of the tiles cut along the contraction, in order, and runs the
+// epilogue: one block per tile and 8 (gated: 16) tokens, 8 outputs per thread.
+template <int kMode>
+__global__ void __launch_bounds__(128) fused_finish(const FusedTcParams p) {
+  using namespace ftc;
+  grid_dependency_wait();
+  constexpr int kTok = kMode == kGated ? 16 : 8, kPer = 128 / kTok;
+  const FusedEpi &e = p.epi;
+  const int t = blockIdx.x;  // among the cut tiles
+  const int64_t total = (int64_t)(p.tiles - p.full) * p.units, u0 = (int64_t)t * p.units, u1 = u0 + p.units;
+  // the CTAs whose ranges [total c / C, total (c + 1) / C) meet [u0, u1)
+  auto begin = [&](int64_t c) { return total * c / p.tail_ctas; };
+  int64_t c0 = u0 * p.tail_ctas / total, c1 = c0;
+  while (begin(c0 + 1) <= u0) ++c0;
+  c1 = c0;
+  while (begin(c1 + 1) < u1) ++c1;
+  if (c0 == c1) return;  // computed whole
+  int row, tok;
+  tile_at(p, p.full + t, row, tok);
+  const int tt = blockIdx.y * kTok + threadIdx.x / kPer, col = 8 * (threadIdx.x % kPer);
+  const int64_t m = (int64_t)tok * p.bn + tt;
+  const int64_t n = kMode == kGated ? (int64_t)row * 64 + col : (int64_t)row * 128 + col;
+  if (tt >= p.bn || m >= e.M || n >= e.N) return;
+  float v[8] = {}, w[8] = {};
+  for (int64_t c = c0; c <= c1; ++c) {
+    const int64_t slot = 2 * c + (begin(c) / p.units == t ? 0 : 1);
+    const float *src = p.part + (slot * p.bn + tt) * 128 + col;
+    float x[8];
+    load8(src, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += x[j];
+    if (kMode == kGated) {
+      load8(src + 64, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] += x[j];
+    }
+  }
+  const float inv = e.tokf[m].y;
+  ColK k;
+  float z[8];
+  k.load(e, kMode == kGrad, n, n, e.N);
+  scale8(v, k, inv, z);
+  if (kMode == kGated) {
+    float u[8];
+    k.load(e, false, e.N + n, n, e.N);
+    scale8(w, k, inv, u);
+    finish_gated(e, m, n, z, u);
+  } else {
+    finish_linear(e, m, n, z);
+  }
+}
+
+template <int kMode>
+cudaError_t launch_fused_tc_mode(const CUtensorMap &tmX, const CUtensorMap &tmP, const FusedTcParams &p, int grid,
+                                 cudaStream_t s) {
+  static std::atomic<int> attr[kAttrDevices];
+  constexpr bool grad = kMode == kGrad;
+  const int smem = ftc::fixed_bytes(grad) + ftc::act_stages(p.bn, grad) * p.bn * ftc::kAct;
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(fused_tc_kernel<kMode>), smem, attr);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(fused_tc_kernel<kMode>, dim3((unsigned)grid), dim3(ftc::kThreads), (size_t)smem, s, tmX, tmP, p);
+  if (e != cudaSuccess || p.full == p.tiles) return e;
+  const int tok = kMode == kGated ? 16 : 8;
+  return launch_pdl(fused_finish<kMode>, dim3((unsigned)(p.tiles - p.full), (unsigned)((p.bn + tok - 1) / tok)), dim3(128),
+                    (size_t)0, s, p);
+}
+
+cudaError_t launch_fused_tc(int mode, const CUtensorMap &tmX, const CUtensorMap &tmP, const FusedTcParams &p, int grid,
+                            cudaStream_t s) {
+  return mode == kLinear  ? launch_fused_tc_mode<kLinear>(tmX, tmP, p, grid, s)
+         : mode == kGated ? launch_fused_tc_mode<kGated>(tmX, tmP, p, grid, s)
+                          : launch_fused_tc_mode<kGrad>(tmX, tmP, p, grid, s);
+}
+
+}  // namespace w4

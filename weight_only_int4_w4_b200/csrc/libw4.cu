@@ -23,7 +23,8 @@
 #include "awq_search.cu"
 #include "outliers.cu"
 #include "gptq.cu"
-#include "fused_simple.cu"
+#include "fused_stage.cu"
+#include "fused_tc.cu"
 #include "w4.h"
 
 namespace w4 {
