@@ -36,7 +36,7 @@ size_t dtype_size(w4_dtype t) { return t == W4_F32 ? 4 : 2; }
 struct FusedPlan {
   int bn = 16, mt = 1, rt = 1, units = 1, gt = 1, full = 0, tiles = 1, tail_ctas = 0, grid = 1;
   int64_t ld = 0;  // row stride of the staged operand
-  size_t xp = 0, tokf = 0, rowf = 0, part = 0, dbias = 0, bytes = 0;
+  size_t xp = 0, tinv = 0, rinv = 0, tab = 0, part = 0, dbias = 0, bytes = 0;
 };
 
 // Fragments of a cut tile hold at least this many 128-deep units.
@@ -63,9 +63,10 @@ bool fused_plan(int64_t M, int64_t N, int64_t K, bool gated, bool grad, int sm, 
   p.grid = p.full > 0 ? std::min(sm, std::max(p.full, p.tail_ctas)) : p.tail_ctas;
   p.ld = grad ? cdiv(N, 8) * 8 : K;
   p.xp = kCounterBytes;
-  p.tokf = p.xp + align256((size_t)M * p.ld * 2);
-  p.rowf = p.tokf + align256((size_t)M * 8);
-  p.part = p.rowf + align256((size_t)N * 8);
+  p.tinv = p.xp + align256((size_t)M * p.ld * 2);
+  p.rinv = p.tinv + align256((size_t)M * 4);
+  p.tab = p.rinv + align256((size_t)N * 4);
+  p.part = p.tab + align256((size_t)N * (K / 32) * 4);  // room for groups of 32
   p.dbias = p.part + align256((size_t)2 * p.tail_ctas * p.bn * 128 * 4);
   const size_t db = !grad ? 0
                           : (size_t)std::max(w4::fused_dbias_ranges(M, N, true), w4::fused_dbias_ranges(M, N, false)) * N * 4;
@@ -141,7 +142,8 @@ w4_status fused_run_tc(const FusedCall &c, const FusedPlan &plan, cudaStream_t s
   if (!enc) return fail(W4_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   uint8_t *ws = static_cast<uint8_t *>(c.workspace);
   uint16_t *xp = reinterpret_cast<uint16_t *>(ws + plan.xp);
-  float2 *tokf = reinterpret_cast<float2 *>(ws + plan.tokf), *rowf = reinterpret_cast<float2 *>(ws + plan.rowf);
+  float *tinv = reinterpret_cast<float *>(ws + plan.tinv), *rinv = reinterpret_cast<float *>(ws + plan.rinv);
+  uint32_t *tab = reinterpret_cast<uint32_t *>(ws + plan.tab);
   const int64_t kg = c.K / c.group, depth = c.grad ? plan.ld : c.K;
   CUtensorMap tmX, tmP;
   CUresult r = encode_2d(enc, &tmX, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xp, (uint64_t)depth, (uint64_t)c.M,
@@ -160,22 +162,23 @@ w4_status fused_run_tc(const FusedCall &c, const FusedPlan &plan, cudaStream_t s
       if (e != cudaSuccess) return cuda_fail(e, "bias gradient launch");
     }
     e = w4::launch_fused_stage_dz(c.X, c.act == W4_ACT_NONE && !c.gated ? nullptr : c.Z, (int)c.x_dtype, (int)c.act,
-                                  c.gated, c.M, c.N, plan.ld, c.scales, kg, xp, tokf, rowf, s);
+                                  c.gated, c.M, c.N, plan.ld, c.scales, c.zeros, kg, xp, tinv, rinv, tab, s);
   } else {
-    e = w4::launch_fused_stage_x(c.X, c.x_dtype == W4_BF16, c.awq_s, c.M, c.K, c.scales, kg, c.N, xp, tokf, rowf, s);
+    e = w4::launch_fused_stage_x(c.X, c.x_dtype == W4_BF16, c.awq_s, c.M, c.K, c.scales, c.zeros, kg, c.N, xp, tinv, rinv,
+                                 tab, s);
   }
   if (e != cudaSuccess) return cuda_fail(e, "operand staging launch");
   w4::FusedTcParams p{};
   p.epi.M = c.M;
   p.epi.N = c.grad ? c.K : c.gated ? c.N / 2 : c.N;
-  p.epi.rowf = rowf; p.epi.tokf = tokf;
+  p.epi.rinv = rinv; p.epi.tinv = tinv;
   p.epi.bias = c.bias;
   p.epi.colmul = c.grad ? c.awq_s : nullptr;
   p.epi.residual = c.residual; p.epi.Z = c.grad ? nullptr : c.Z; p.epi.Y = c.Y;
   p.epi.act = c.grad ? (int)W4_ACT_NONE : (int)c.act;
   p.epi.z_dtype = (int)c.x_dtype; p.epi.y_dtype = (int)c.y_dtype;
   p.epi.vec = p.epi.N % 8 == 0;
-  p.scales = c.scales; p.zeros = c.zeros;
+  p.tab = tab;
   p.rows = c.N; p.kg = kg;
   p.gshift = c.group == 128 ? 7 : c.group == 64 ? 6 : 5;
   p.bn = plan.bn; p.mt = plan.mt; p.rt = plan.rt; p.units = plan.units; p.gt = plan.gt;

@@ -37,14 +37,46 @@ __device__ __forceinline__ float block_max(float v, float *red) {
   return v;
 }
 
-// One warp: the row factors (r, 1 / r) of packed row n.
-__device__ __forceinline__ void row_factor(const uint16_t *scales, int64_t kg, int64_t n, float2 *rowf) {
-  const int lane = threadIdx.x & 31;
-  float mx = 0.0f;
-  for (int64_t g = lane; g < kg; g += 32) mx = fmaxf(mx, half_bits_to_float(scales[n * kg + g]));
+// Row factors and group constants of 32 packed rows (256 threads): rinv[n] = 1 / r and,
+// transposed to [group][row], the fp16 pair (scale * r, 1024 + z).  Rows are the lanes of
+// every kernel that dequantizes, so a warp then reads its constants as one 128-byte line;
+// straight from scales [n][g] each lane touched a line of its own, and the lines of a
+// tile did not fit L1.
+constexpr int kPrepRows = 32;
+
+__device__ __forceinline__ void prep_rows(const uint16_t *scales, const uint16_t *zeros, int64_t kg, int64_t N, int64_t n0,
+                                          float *rinv, uint32_t *tab) {
+  __shared__ uint32_t tile[kPrepRows][33];
+  __shared__ float rr[kPrepRows];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-  if (lane == 0) rowf[n] = pow2_to(mx, 10);
+  for (int i = 0; i < 4; ++i) {
+    const int64_t n = n0 + 4 * w + i;
+    float mx = 0.0f;
+    if (n < N)
+      for (int64_t g = lane; g < kg; g += 32) mx = fmaxf(mx, half_bits_to_float(scales[n * kg + g]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+    const float2 f = pow2_to(mx, 10);
+    if (lane == 0) rr[4 * w + i] = f.x;
+    if (lane == 0 && n < N) rinv[n] = f.y;
+  }
+  __syncwarp();  // a warp converts the rows whose factors it found
+  for (int64_t g0 = 0; g0 < kg; g0 += 32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t n = n0 + 4 * w + i, g = g0 + lane;
+      if (n < N && g < kg) {
+        const __half2 h = __floats2half2_rn(half_bits_to_float(scales[n * kg + g]) * rr[4 * w + i],
+                                            1024.0f + half_bits_to_float(zeros[n * kg + g]));
+        tile[4 * w + i][lane] = *reinterpret_cast<const uint32_t *>(&h);
+      }
+    }
+    __syncthreads();
+    for (int gi = w; gi < 32; gi += 8)
+      if (g0 + gi < kg && n0 + lane < N) tab[(g0 + gi) * N + n0 + lane] = tile[lane][gi];
+    __syncthreads();
+  }
 }
 
 template <bool kBf16>
@@ -69,8 +101,8 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
 }
 
 // Blocks 0..M-1: x' = fp16(x s e) of one token, in the order the dequantization yields
-// (0, 4, 1, 5, 2, 6, 3, 7 of every 8 channels), and (e, 1 / e).  The blocks behind them:
-// the row factors, one warp per packed row.  A token is read once: each thread keeps up
+// (0, 4, 1, 5, 2, 6, 3, 7 of every 8 channels), and 1 / e.  The blocks behind them:
+// row factors and group constants of 32 packed rows each.  A token is read once: each thread keeps up
 // to 4 vectors (K <= 8192 at 256 threads) between the maximum and the conversion; deeper
 // layers read the rest again, from L1 or L2.
 constexpr int kStageThreads = 256;
@@ -78,12 +110,11 @@ constexpr int kStageKeep = 4;
 
 template <bool kBf16>
 __global__ void __launch_bounds__(kStageThreads)
-    fused_stage_x(const uint16_t *X, const float *awq_s, int64_t M, int64_t K, const uint16_t *scales, int64_t kg,
-                  int64_t N, uint16_t *xp, float2 *tokf, float2 *rowf) {
+    fused_stage_x(const uint16_t *X, const float *awq_s, int64_t M, int64_t K, const uint16_t *scales,
+                  const uint16_t *zeros, int64_t kg, int64_t N, uint16_t *xp, float *tinv, float *rinv, uint32_t *tab) {
   grid_launch_dependents();
   if (blockIdx.x >= M) {
-    const int64_t n = ((int64_t)blockIdx.x - M) * (kStageThreads / 32) + (threadIdx.x >> 5);
-    if (n < N) row_factor(scales, kg, n, rowf);
+    prep_rows(scales, zeros, kg, N, ((int64_t)blockIdx.x - M) * kPrepRows, rinv, tab);
     return;
   }
   __shared__ float red[kStageThreads / 32];
@@ -120,7 +151,7 @@ __global__ void __launch_bounds__(kStageThreads)
     for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(f[j]));
   }
   const float2 e = pow2_to(block_max(mx, red), 13);
-  if (threadIdx.x == 0) tokf[m] = e;
+  if (threadIdx.x == 0) tinv[m] = e.y;
   uint4 *out = reinterpret_cast<uint4 *>(xp + m * K);
   auto put = [&](const uint4 &w, int64_t v) {
     float f[8];
@@ -137,10 +168,9 @@ __global__ void __launch_bounds__(kStageThreads)
 }
 
 __global__ void __launch_bounds__(kStageThreads)
-    fused_row_factors(const uint16_t *scales, int64_t kg, int64_t N, float2 *rowf) {
+    fused_prep(const uint16_t *scales, const uint16_t *zeros, int64_t kg, int64_t N, float *rinv, uint32_t *tab) {
   grid_launch_dependents();
-  const int64_t n = (int64_t)blockIdx.x * (kStageThreads / 32) + (threadIdx.x >> 5);
-  if (n < N) row_factor(scales, kg, n, rowf);
+  prep_rows(scales, zeros, kg, N, (int64_t)blockIdx.x * kPrepRows, rinv, tab);
 }
 
 // dZ of `kVec` consecutive rows n.. of token m (gated: n.. lies on one side of F).
@@ -170,11 +200,11 @@ __device__ __forceinline__ void dz_at(const void *dY, const void *Z, int dtype, 
 }
 
 // dz' = fp16(dZ / r[n] * e) of one token per block, natural order, columns N.. up to the
-// row stride `ld` zero, and (e, 1 / e).  Two passes: the second finds its inputs in L2.
+// row stride `ld` zero, and 1 / e.  Two passes: the second finds its inputs in L2.
 template <bool kGated, int kVec>
 __global__ void __launch_bounds__(512)
-    fused_stage_dz(const void *dY, const void *Z, int dtype, int act, int64_t N, int64_t ld, const float2 *rowf,
-                   uint16_t *dzp, float2 *tokf) {
+    fused_stage_dz(const void *dY, const void *Z, int dtype, int act, int64_t N, int64_t ld, const float *rinv,
+                   uint16_t *dzp, float *tinv) {
   grid_launch_dependents();
   grid_dependency_wait();  // the row factors
   __shared__ float red[16];
@@ -184,16 +214,16 @@ __global__ void __launch_bounds__(512)
     float d[kVec];
     dz_at<kGated, kVec>(dY, Z, dtype, act, N, m, n, d);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) mx = fmaxf(mx, fabsf(d[j] * rowf[n + j].y));
+    for (int j = 0; j < kVec; ++j) mx = fmaxf(mx, fabsf(d[j] * rinv[n + j]));
   }
   const float2 e = pow2_to(block_max(mx, red), 13);
-  if (threadIdx.x == 0) tokf[m] = e;
+  if (threadIdx.x == 0) tinv[m] = e.y;
   for (int64_t n = (int64_t)threadIdx.x * kVec; n < ld; n += 512 * kVec) {
     float d[kVec] = {};
     if (n < N) {
       dz_at<kGated, kVec>(dY, Z, dtype, act, N, m, n, d);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) d[j] = d[j] * rowf[n + j].y * e.x;
+      for (int j = 0; j < kVec; ++j) d[j] = d[j] * rinv[n + j] * e.x;
     }
     if constexpr (kVec == 8)
       *reinterpret_cast<uint4 *>(dzp + m * ld + n) = make_uint4(half2_bits(d[0], d[1]), half2_bits(d[2], d[3]),
@@ -259,27 +289,26 @@ cudaError_t launch_pdl(void (*kern)(Args...), dim3 grid, dim3 block, size_t smem
 }
 
 cudaError_t launch_fused_stage_x(const void *X, bool bf16, const float *awq_s, int64_t M, int64_t K,
-                                 const uint16_t *scales, int64_t kg, int64_t N, uint16_t *xp, float2 *tokf, float2 *rowf,
-                                 cudaStream_t s) {
-  const unsigned grid = (unsigned)(M + (N + kStageThreads / 32 - 1) / (kStageThreads / 32));
+                                 const uint16_t *scales, const uint16_t *zeros, int64_t kg, int64_t N, uint16_t *xp,
+                                 float *tinv, float *rinv, uint32_t *tab, cudaStream_t s) {
+  const unsigned grid = (unsigned)(M + (N + kPrepRows - 1) / kPrepRows);
   const uint16_t *x = static_cast<const uint16_t *>(X);
-  if (bf16) fused_stage_x<true><<<grid, kStageThreads, 0, s>>>(x, awq_s, M, K, scales, kg, N, xp, tokf, rowf);
-  else fused_stage_x<false><<<grid, kStageThreads, 0, s>>>(x, awq_s, M, K, scales, kg, N, xp, tokf, rowf);
+  if (bf16) fused_stage_x<true><<<grid, kStageThreads, 0, s>>>(x, awq_s, M, K, scales, zeros, kg, N, xp, tinv, rinv, tab);
+  else fused_stage_x<false><<<grid, kStageThreads, 0, s>>>(x, awq_s, M, K, scales, zeros, kg, N, xp, tinv, rinv, tab);
   return cudaGetLastError();
 }
 
 cudaError_t launch_fused_stage_dz(const void *dY, const void *Z, int dtype, int act, bool gated, int64_t M, int64_t N,
-                                  int64_t ld, const uint16_t *scales, int64_t kg, uint16_t *dzp, float2 *tokf,
-                                  float2 *rowf, cudaStream_t s) {
-  fused_row_factors<<<(unsigned)((N + kStageThreads / 32 - 1) / (kStageThreads / 32)), kStageThreads, 0, s>>>(
-      scales, kg, N, rowf);
+                                  int64_t ld, const uint16_t *scales, const uint16_t *zeros, int64_t kg, uint16_t *dzp,
+                                  float *tinv, float *rinv, uint32_t *tab, cudaStream_t s) {
+  fused_prep<<<(unsigned)((N + kPrepRows - 1) / kPrepRows), kStageThreads, 0, s>>>(scales, zeros, kg, N, rinv, tab);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // 16-byte vectors where every row (and its gated half) starts on one
   const bool vec = (gated ? N / 2 : N) % 8 == 0;
   auto k = gated ? (vec ? fused_stage_dz<true, 8> : fused_stage_dz<true, 1>)
                  : (vec ? fused_stage_dz<false, 8> : fused_stage_dz<false, 1>);
-  return launch_pdl(k, dim3((unsigned)M), dim3(512), 0, s, dY, Z, dtype, act, N, ld, (const float2 *)rowf, dzp, tokf);
+  return launch_pdl(k, dim3((unsigned)M), dim3(512), 0, s, dY, Z, dtype, act, N, ld, (const float *)rinv, dzp, tinv);
 }
 
 // Token ranges of dbias: about four blocks per SM, at least 8 tokens each.

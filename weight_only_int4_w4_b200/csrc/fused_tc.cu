@@ -7,9 +7,9 @@
 // gate rows and the 64 up rows that belong to them, so that act(G) * U is formed in the
 // tile's epilogue and neither G nor U goes to memory (unless they are asked for).
 //
-// Roles (512 threads): warp 0 loads activations (TMA), warp 1 loads codes (TMA), warp 2
-// issues the MMAs, warp 3 owns TMEM, warps 4..7 write results, warps 8..15 dequantize in
-// two sets of four that take turns.  The MMA and TMA instructions sit under elect.sync in
+// Roles (640 threads): warp 0 loads activations (TMA), warp 1 loads codes (TMA), warp 2
+// issues the MMAs, warp 3 owns TMEM, warps 4..7 write results, warps 8..19 dequantize in
+// three sets of four that take turns, a 64-deep block each.  The MMA and TMA instructions sit under elect.sync in
 // warp-uniform code: issued from a thread-dependent branch, each one costs the issuing
 // thread about 78 ns for operands moved to uniform registers one by one, whatever its
 // size (measured; 4 x 128x256x16 in 313 ns instead of 280).
@@ -38,8 +38,8 @@ enum FusedMode { kLinear = 0, kGated = 1, kGrad = 2 };
 
 struct FusedEpi {
   int64_t M, N;             // tokens, output columns of a linear / gradient call, F of a gated one
-  const float2 *rowf;       // forward: (r, 1 / r) per packed row
-  const float2 *tokf;       // (e, 1 / e) per token
+  const float *rinv;        // 1 / r per packed row
+  const float *tinv;        // 1 / e per token
   const float *bias;        // forward, or NULL
   const float *colmul;      // gradient: awq_s, or NULL
   const void *residual;     // or NULL
@@ -49,7 +49,7 @@ struct FusedEpi {
 
 struct FusedTcParams {
   FusedEpi epi;
-  const uint16_t *scales, *zeros;
+  const uint32_t *tab;      // [kg][rows] fp16 pairs (scale * r, 1024 + z)
   int64_t rows;             // packed rows
   int64_t kg;               // groups per packed row
   int gshift;               // log2(group)
@@ -62,16 +62,17 @@ struct FusedTcParams {
 
 namespace ftc {
 
-constexpr int kThreads = 512;
+constexpr int kSets = 3;                 // dequantizing sets of four warps, one A buffer each
+constexpr int kThreads = 256 + kSets * 128;
 constexpr int kCodeStages = 4, kCodeStage = 128 * 64;
 constexpr int kAct = 64 * 2;             // bytes of a token's 64 channels in a stage
 constexpr int kStageOut = 32 * 128 * 4;  // 32 tokens of a tile in fp32
-constexpr int kGradA = 3, kGradAStage = 64 * 128 * 2;
+constexpr int kGradAStage = 64 * 128 * 2;
 constexpr int kMaxBn = 208;
 constexpr int kMaxActStages = 8;
 
 __host__ __device__ constexpr int fixed_bytes(bool grad) {
-  return 1024 + kCodeStages * kCodeStage + 2 * kStageOut + (grad ? kGradA * kGradAStage : 0) + 2 * 256 * 4 + 512;
+  return 1024 + kCodeStages * kCodeStage + 2 * kStageOut + (grad ? kSets * kGradAStage : 0) + 2 * 256 * 4 + 512;
 }
 __host__ __device__ inline int act_stages(int bn, bool grad) {
   const int n = (227 * 1024 - fixed_bytes(grad)) / (bn * kAct);
@@ -126,19 +127,21 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
                             *reinterpret_cast<const __half2 *>(&c));
   return *reinterpret_cast<const uint32_t *>(&r);
 }
-__device__ __forceinline__ uint32_t dup_half(float v) {
-  const __half2 h = __float2half2_rn(v);
-  return *reinterpret_cast<const uint32_t *>(&h);
+
+// A volatile load, which stays where it is written: a whole block ahead of its use.
+__device__ __forceinline__ uint32_t ldg_const(const uint32_t *p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
 }
 
 // A group's constants as fp16 pairs: scale * r, 1024 + z, -(64 + z).
 struct GroupK {
   uint32_t s, zlo, zhi;
-  __device__ __forceinline__ void set(uint16_t scale, uint16_t zero, float r) {
-    const float z = half_bits_to_float(zero);
-    s = dup_half(half_bits_to_float(scale) * r);
-    zlo = dup_half(1024.0f + z);
-    zhi = dup_half(-64.0f - z);
+  __device__ __forceinline__ void set(uint32_t w) {
+    s = __byte_perm(w, w, 0x1010);
+    zlo = __byte_perm(w, w, 0x3232);
+    zhi = hsub2(0x63806380u, zlo);  // 960 - (1024 + z)
   }
 };
 
@@ -256,7 +259,7 @@ struct ColK {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const bool ok = n + j < lim;
-      f[j] = !ok ? 0.0f : grad ? (e.colmul ? e.colmul[first + j] : 1.0f) : e.rowf[first + j].y;
+      f[j] = !ok ? 0.0f : grad ? (e.colmul ? e.colmul[first + j] : 1.0f) : e.rinv[first + j];
       b[j] = ok && e.bias ? e.bias[first + j] : 0.0f;
     }
   }
@@ -317,32 +320,25 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
   uint8_t *sC = smem;
   float *sOut = reinterpret_cast<float *>(sC + kCodeStages * kCodeStage);
   uint8_t *sA = reinterpret_cast<uint8_t *>(sOut) + 2 * kStageOut;
-  uint8_t *sX = sA + (kIsGrad ? kGradA * kGradAStage : 0);
+  uint8_t *sX = sA + (kIsGrad ? kSets * kGradAStage : 0);
   float *sTok = reinterpret_cast<float *>(sX + ns * act_stage);
   uint64_t *bars = reinterpret_cast<uint64_t *>(sTok + 256);
-  uint64_t *xfull = bars, *xempty = xfull + kMaxActStages;
-  uint64_t *cfull = xempty + kMaxActStages, *cempty = cfull + kCodeStages;
-  uint64_t *afull = cempty + kCodeStages, *aempty = afull + 8;
-  uint64_t *dfull = aempty + 8, *dempty = dfull + 2;
+  uint64_t *full = bars, *empty = full + kMaxActStages;
+  uint64_t *cfull = empty + kMaxActStages, *cempty = cfull + kCodeStages;
+  uint64_t *dfull = cempty + kCodeStages, *dempty = dfull + 2;
   uint32_t *holder = reinterpret_cast<uint32_t *>(dempty + 2);
 
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
-  // A buffers: TMEM columns behind the two accumulators, or shared memory
-  const int na = kIsGrad ? kGradA : min(8, (512 - 2 * p.bn) / 32);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < ns; ++i) {
-      mbar_init(&xfull[i], 1);
-      mbar_init(&xempty[i], 1);
+      mbar_init(&full[i], 1 + 128);  // the activations' box, and the set that converts the block
+      mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < kCodeStages; ++i) {
       mbar_init(&cfull[i], 1);
-      mbar_init(&cempty[i], 128);
-    }
-    for (int i = 0; i < na; ++i) {
-      mbar_init(&afull[i], 128);
-      mbar_init(&aempty[i], 1);
+      mbar_init(&cempty[i], 256);  // a unit's two blocks, a set each
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&dfull[i], 1);
@@ -373,10 +369,10 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
       int row, tok;
       tile_at(p, tile, row, tok);
       for (int b = 2 * k0; b < 2 * k1; ++b) {
-        if (!wait_all(&xempty[s], ph ^ 1u, kErrTimeoutTma)) { ok = false; break; }
+        if (!wait_all(&empty[s], ph ^ 1u, kErrTimeoutTma)) { ok = false; break; }
         if (elect_one()) {
-          mbar_arrive_expect_tx(&xfull[s], (uint32_t)act_stage);
-          tma_load_2d(sX + s * act_stage, &tmX, &xfull[s], b * 64, tok * p.bn);
+          mbar_arrive_expect_tx(&full[s], (uint32_t)act_stage);
+          tma_load_2d(sX + s * act_stage, &tmX, &full[s], b * 64, tok * p.bn);
         }
         __syncwarp();
         if (++s == ns) s = 0, ph ^= 1u;
@@ -411,19 +407,19 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
     // ---- products
     const uint32_t idesc = idesc_f16(false, p.bn) | (kIsGrad ? 1u << 15 : 0u);  // bit 15: A is MN-major
     int s = 0, a = 0, d = 0;
-    uint32_t xph = 0, aph = 0, dph = 0;
+    uint32_t ph = 0, dph = 0;
+    bool ready = false;  // the barrier of the block at hand was seen complete while the last one was issued
     while (ok && work.next(tile, k0, k1, slot)) {
       if (!wait_all(&dempty[d], dph ^ 1u, kErrTimeoutMma)) { ok = false; break; }
       tc_fence_after();
       const uint32_t acc = tmem + (uint32_t)(d * p.bn);
       for (int b = 2 * k0; b < 2 * k1; ++b) {
-        if (!wait_all(&xfull[s], xph, kErrTimeoutMma) || !wait_all(&afull[a], aph, kErrTimeoutMma)) {
-          ok = false;
-          break;
-        }
+        if (!ready && !wait_all(&full[s], ph, kErrTimeoutMma)) { ok = false; break; }
         tc_fence_after();
         const uint64_t bd = smem_desc_k_sw128(smem_u32(sX + s * act_stage));
-        const bool first = b == 2 * k0;
+        uint64_t *done = &empty[s];
+        if (++s == ns) s = 0, ph ^= 1u;
+        ready = __all_sync(~0u, mbar_try_wait(&full[s], ph));
         if (elect_one()) {
           if constexpr (kIsGrad) {
             // MN-major A: 64-channel halves 8192 bytes apart (leading offset), 8-row
@@ -432,136 +428,121 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
                                 ((uint64_t)(8192 >> 4) << 16);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              tc_mma_ss(acc, ad + (uint64_t)(128 * j), bd + (uint64_t)(2 * j), idesc, first && j == 0 ? 0u : 1u);
+              tc_mma_ss(acc, ad + (uint64_t)(128 * j), bd + (uint64_t)(2 * j), idesc, b == 2 * k0 && j == 0 ? 0u : 1u);
           } else {
             const uint32_t at = tmem + (uint32_t)(2 * p.bn + 32 * a);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              tc_mma_ts(acc, at + 8 * j, bd + (uint64_t)(2 * j), idesc, first && j == 0 ? 0u : 1u);
+              tc_mma_ts(acc, at + 8 * j, bd + (uint64_t)(2 * j), idesc, b == 2 * k0 && j == 0 ? 0u : 1u);
           }
-          tc_commit(&xempty[s]);
-          tc_commit(&aempty[a]);
+          tc_commit(done);
           if (b == 2 * k1 - 1) tc_commit(&dfull[d]);
         }
         __syncwarp();
-        if (++s == ns) s = 0, xph ^= 1u;
-        if (++a == na) a = 0, aph ^= 1u;
+        if (++a == kSets) a = 0;
       }
       d ^= 1;
       if (d == 0) dph ^= 1u;
     }
   } else if (warp >= 8) {
-    // ---- dequantization: set (warp - 8) / 4 takes every other unit
+    // ---- dequantization: set j takes blocks j, j + 3, ... of the CTA's whole sequence and
+    // owns A buffer j, so it converts a block while the other sets' blocks are multiplied
     const int set = (warp - 8) >> 2, wq = warp & 3;
-    grid_dependency_wait();  // the row factors
-    int i = 0;               // units seen by both sets
-    while (ok && work.next(tile, k0, k1, slot)) {
-      int row, tok;
-      tile_at(p, tile, row, tok);
-      // forward: this thread's packed row, TMEM lane 32 wq + lane; its group constants are
-      // fetched one unit ahead (of this set's)
-      const int r = 32 * wq + lane;
-      int64_t n = 0;
-      bool row_ok = true;
-      float rf = 0.0f;
-      if constexpr (!kIsGrad) {
-        if (kMode == kLinear) {
+    grid_dependency_wait();  // the group constants
+    // forward: this thread's packed row, TMEM lane r = 32 wq + lane
+    // gradient: row nl of the block (of the contraction), channel half kh
+    const int r = 32 * wq + lane, nl = 32 * (wq & 1) + lane, kh = wq >> 1;
+    // The next block of this set: its constants (two 32-channel pieces) are fetched a
+    // whole block of this set's ahead, across the ends of tiles.
+    int b = set, b1 = 0;  // place in the current range of blocks, its end
+    int64_t n = 0;
+    int row = 0;
+    bool row_ok = false;
+    uint32_t gw[2];
+    auto seek = [&]() -> bool {  // moves to the range that holds block b
+      while (b >= b1) {
+        b -= b1;
+        if (!work.next(tile, k0, k1, slot)) return false;
+        int tok;
+        tile_at(p, tile, row, tok);
+        b += 2 * k0;
+        b1 = 2 * k1;
+        if constexpr (kMode == kLinear) {
           n = (int64_t)row * 128 + r;
           row_ok = n < p.rows;
-        } else {
+        } else if constexpr (kMode == kGated) {
           const int64_t f = (int64_t)row * 64 + (r & 63);
           n = r < 64 ? f : p.epi.N + f;
           row_ok = f < p.epi.N;
         }
-        rf = row_ok ? p.epi.rowf[n].x : 0.0f;
       }
-      // gradient: rows n of the contraction, two per unit (blocks of 64), channel half kh
-      const int nl = 32 * (wq & 1) + lane, kh = wq >> 1;
-      uint16_t sc[4], zc[4];  // forward: 32-channel pieces of a unit; gradient: [block][32-channel piece]
-      float rfs[2] = {0.0f, 0.0f};
-      auto fetch = [&](int u) {
-        if constexpr (kIsGrad) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int64_t nn = (int64_t)u * 128 + h * 64 + nl;
-            const bool in = nn < p.rows;
-            rfs[h] = in ? p.epi.rowf[nn].x : 0.0f;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int64_t g = ((int64_t)row * 128 + kh * 64 + c * 32) >> p.gshift;
-              const bool gin = in && g < p.kg;
-              sc[2 * h + c] = gin ? __ldg(p.scales + nn * p.kg + g) : (uint16_t)0;
-              zc[2 * h + c] = gin ? __ldg(p.zeros + nn * p.kg + g) : (uint16_t)0;
-            }
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (c > 0 && p.gshift == 7) {
-              sc[c] = sc[0];
-              zc[c] = zc[0];
-              continue;
-            }
-            const int64_t g = ((int64_t)u * 128 + c * 32) >> p.gshift;
-            const bool in = row_ok && g < p.kg;
-            sc[c] = in ? __ldg(p.scales + n * p.kg + g) : (uint16_t)0;
-            zc[c] = in ? __ldg(p.zeros + n * p.kg + g) : (uint16_t)0;
-          }
-        }
-      };
-      const int first = k0 + ((i + set) & 1);  // this set's first unit of the range
-      if (first < k1) fetch(first);
-      for (int u = first; u < k1; u += 2) {
-        const int iu = i + (u - k0);
-        const int s = iu % kCodeStages;
-        GroupK g[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) g[c].set(sc[c], zc[c], kIsGrad ? rfs[c >> 1] : rf);
-        if (u + 2 < k1) fetch(u + 2);
-        if (!wait_all(&cfull[s], (uint32_t)(iu / kCodeStages) & 1u, kErrTimeoutDequant)) { ok = false; break; }
-        const uint32_t src = smem_u32(sC + s * kCodeStage);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int ia = 2 * iu + h, a = ia % na;
-          // forward: row r, chunks 2h, 2h + 1;  gradient: row 64 h + nl, chunks 2 kh, 2 kh + 1
-          const int cr = kIsGrad ? 64 * h + nl : r, cc = kIsGrad ? 2 * kh : 2 * h;
-          const uint32_t base = src + (uint32_t)(cr * 64), sw = (uint32_t)((cr >> 1) & 3);
-          const uint4 q0 = lds128(base + ((((uint32_t)cc) ^ sw) << 4));
-          const uint4 q1 = lds128(base + ((((uint32_t)cc + 1u) ^ sw) << 4));
-          const uint32_t wd[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-          uint32_t out[32];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint32_t o[4];
-            // constants: forward piece 2h + (j / 4) of the unit, gradient [h][j / 4]
-            dequant8(wd[j], g[2 * h + (j >> 2)], o);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) out[4 * j + x] = o[x];
-          }
-          if (!wait_all(&aempty[a], ((uint32_t)(ia / na) & 1u) ^ 1u, kErrTimeoutDequant)) { ok = false; break; }
-          if constexpr (kIsGrad) {
-            const uint32_t dst = smem_u32(sA + a * kGradAStage) + (uint32_t)(kh * 8192 + nl * 128);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (uint32_t)((j ^ (nl & 7)) << 4)),
-                           "r"(out[4 * j]), "r"(out[4 * j + 1]), "r"(out[4 * j + 2]), "r"(out[4 * j + 3])
-                           : "memory");
-            fence_proxy_async_smem();
-          } else {
-            tc_fence_after();
-            tmem_st_32x32b_x32(tmem + ((uint32_t)(32 * wq) << 16) + (uint32_t)(2 * p.bn + 32 * a), out);
-            tc_wait_st();
-            tc_fence_before();
-          }
-          mbar_arrive(&afull[a]);
-        }
-        if (!ok) break;
-        // The codes are given back only here, behind the stores that needed them: an arrive
-        // right behind the loads let the loads sink below it, and now and then read the
-        // stage's next contents.
-        mbar_arrive(&cempty[s]);
+      return true;
+    };
+    auto fetch = [&]() {
+      if constexpr (kIsGrad) {
+        n = (int64_t)b * 64 + nl;
+        row_ok = n < p.rows;
       }
-      i += k1 - k0;
+      const int64_t ch = kIsGrad ? (int64_t)row * 128 + 64 * kh : (int64_t)b * 64;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {  // two loads even where both pieces are in one group: a
+        // copy of the first one's value would wait for it here
+        const int64_t g = (ch + 32 * c) >> p.gshift;
+        gw[c] = row_ok && g < p.kg ? ldg_const(p.tab + g * p.rows + n) : 0u;
+      }
+    };
+    bool more = seek();
+    if (more) fetch();
+    int s = set, ps = 0;  // ring stage of the block, and of this set's last one
+    uint32_t sph = 0, pph = 0;
+    for (int ia = set; more; ia += kSets) {
+      const int cs = (ia >> 1) % kCodeStages, h = ia & 1;
+      if (!wait_all(&cfull[cs], (uint32_t)((ia >> 1) / kCodeStages) & 1u, kErrTimeoutDequant)) { ok = false; break; }
+      // forward: row r, chunks 2h, 2h + 1;  gradient: row 64 h + nl, chunks 2 kh, 2 kh + 1
+      const int cr = kIsGrad ? 64 * h + nl : r, cc = kIsGrad ? 2 * kh : 2 * h;
+      const uint32_t base = smem_u32(sC + cs * kCodeStage) + (uint32_t)(cr * 64), sw = (uint32_t)((cr >> 1) & 3);
+      const uint4 q0 = lds128(base + ((((uint32_t)cc) ^ sw) << 4));
+      const uint4 q1 = lds128(base + ((((uint32_t)cc + 1u) ^ sw) << 4));
+      GroupK g[2];
+      g[0].set(gw[0]);
+      g[1].set(gw[1]);
+      b += kSets;
+      more = seek();
+      if (more) fetch();
+      const uint32_t wd[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+      uint32_t out[32];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t o[4];
+        dequant8(wd[j], g[j >> 2], o);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) out[4 * j + x] = o[x];
+      }
+      // the buffer is free once this set's last block has been multiplied
+      if (ia >= kSets && !wait_all(&empty[ps], pph, kErrTimeoutDequant)) { ok = false; break; }
+      if constexpr (kIsGrad) {
+        const uint32_t dst = smem_u32(sA + set * kGradAStage) + (uint32_t)(kh * 8192 + nl * 128);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (uint32_t)((j ^ (nl & 7)) << 4)),
+                       "r"(out[4 * j]), "r"(out[4 * j + 1]), "r"(out[4 * j + 2]), "r"(out[4 * j + 3])
+                       : "memory");
+        fence_proxy_async_smem();
+      } else {
+        tc_fence_after();
+        tmem_st_32x32b_x32(tmem + ((uint32_t)(32 * wq) << 16) + (uint32_t)(2 * p.bn + 32 * set), out);
+        tc_wait_st();
+        tc_fence_before();
+      }
+      mbar_arrive(&full[s]);
+      // The codes are given back only here, behind the stores that needed them: an arrive
+      // right behind the loads let the loads sink below it, and now and then read the
+      // stage's next contents.
+      mbar_arrive(&cempty[cs]);
+      ps = s;
+      pph = sph;
+      s += kSets;
+      if (s >= ns) s -= ns, sph ^= 1u;
     }
   } else if (warp >= 4) {
     // ---- epilogue
@@ -574,7 +555,7 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
       int row, tok;
       tile_at(p, tile, row, tok);
       const int64_t m0 = (int64_t)tok * p.bn;
-      for (int t = tid; t < p.bn; t += 128) sTok[t] = m0 + t < e.M ? e.tokf[m0 + t].y : 0.0f;
+      for (int t = tid; t < p.bn; t += 128) sTok[t] = m0 + t < e.M ? e.tinv[m0 + t] : 0.0f;
       ColK c0, c1;
       const int64_t n = kMode == kGated ? (int64_t)row * 64 + 8 * (tid & 7) : (int64_t)row * 128 + 8 * (tid & 15);
       if (slot < 0) {
@@ -690,7 +671,7 @@ __global__ void __launch_bounds__(128) fused_finish(const FusedTcParams p) {
       for (int j = 0; j < 8; ++j) w[j] += x[j];
     }
   }
-  const float inv = e.tokf[m].y;
+  const float inv = e.tinv[m];
   ColK k;
   float z[8];
   k.load(e, kMode == kGrad, n, n, e.N);
