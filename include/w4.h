@@ -404,11 +404,12 @@ typedef enum {
  *   Y         device [M][N], F32, F16 or BF16
  *   group     32, 64 or 128; K a multiple of the group and of 64
  *   packed, scales, zeros, awq_s   as for w4a16_gemm
- *   workspace device scratch of w4a16_linear_workspace_size(M, N, K) bytes, zero-
- *             filled before its first use, under the same rule as w4a16_gemm's:
- *             the first 128 KiB are left zero by every call, the rest holds nothing
- *             between calls, and calls that share it must not overlap in time.
- *             The operators of this header may share one workspace.
+ *   workspace device scratch of w4a16_linear_workspace_size(M, N, K) bytes.  It
+ *             need not be zeroed and holds nothing between calls; its first 128
+ *             KiB are not touched, so that one buffer may serve w4a16_gemm (whose
+ *             counters lie there) and the fused operators in turn.  Calls that
+ *             share it must not overlap in time.  With at most 16 tokens and
+ *             group 128 none is needed, and NULL may be given.
  * Z is accumulated in fp32; bias, activation and residual are applied in fp32 and
  * each output is rounded once.  W^ (and, with awq_s, x * s) may be rounded to fp16
  * once before the product.  A token with an infinity or NaN among its activations

@@ -74,6 +74,28 @@ bool fused_plan(int64_t M, int64_t N, int64_t K, bool gated, bool grad, int sm, 
   return true;
 }
 
+// Up to 16 tokens on groups of 128: one kernel, no workspace.  Splits K over as many of a
+// CTA's 16 warps as there are pieces of channels and room for the partial sums; CTAs are
+// as many as SMs, or a multiple where their rows' partial sums would not fit.
+struct GemvFusedPlan {
+  int grid = 0, ksw = 1, nblk = 1;
+};
+bool fused_gemv_plan(int64_t M, int64_t N, int64_t K, int group, bool gated, int sm, GemvFusedPlan &p) {
+  if (group != w4::kGroup || M > w4::fgv::kMaxTokens) return false;
+  const int64_t out = gated ? N / 2 : N, pieces = cdiv(K / w4::kGroup, M <= 8 ? 2 : 1);
+  for (int64_t grid = std::min<int64_t>(sm, cdiv(out, 8)); grid <= (int64_t)1 << 20; grid *= 2) {
+    const int64_t nblk = cdiv(cdiv(out, grid), 16) * (gated ? 2 : 1);
+    for (int ksw = 16; ksw >= 1; ksw /= 2) {
+      if (ksw > pieces || w4::fgv::smem_bytes(ksw, 1, (int)M) * nblk > w4::fgv::kSmemMax) continue;
+      p.grid = (int)grid;
+      p.ksw = ksw;
+      p.nblk = (int)nblk;
+      return true;
+    }
+  }
+  return false;
+}
+
 int sm_count_or_b200() {
   int sm = 0;
   return current_sm_count(&sm) == cudaSuccess ? sm : 148;
@@ -129,7 +151,10 @@ w4_status fused_check(const FusedCall &c) {
   for (int i = 0; i < 8; ++i)
     if (overlap(c.workspace, c.workspace_bytes, ins[i].p, ins[i].n))
       return fail(W4_ERR_INVALID_ARG, "the workspace overlaps an input");
-  const size_t need = fused_ws_bytes(c.M, c.N, c.K, c.gated, c.grad);
+  GemvFusedPlan gv;
+  const size_t need = !c.grad && fused_gemv_plan(c.M, c.N, c.K, c.group, c.gated, sm_count_or_b200(), gv)
+                          ? 0
+                          : fused_ws_bytes(c.M, c.N, c.K, c.gated, c.grad);
   if (need > 0 && (!c.workspace || c.workspace_bytes < need))
     return fail(W4_ERR_INVALID_ARG, "workspace too small: need %zu bytes, got %zu", need,
                 c.workspace ? c.workspace_bytes : (size_t)0);
@@ -189,6 +214,19 @@ w4_status fused_run_tc(const FusedCall &c, const FusedPlan &plan, cudaStream_t s
   return W4_OK;
 }
 
+w4_status fused_run_gemv(const FusedCall &c, const GemvFusedPlan &plan, cudaStream_t s) {
+  w4::FusedGemvParams p{};
+  p.X = static_cast<const uint16_t *>(c.X);
+  p.M = c.M; p.N = c.gated ? c.N / 2 : c.N; p.K = c.K;
+  p.packed = c.packed; p.scales = c.scales; p.zeros = c.zeros; p.awq_s = c.awq_s;
+  p.epi.bias = c.bias; p.epi.residual = c.residual; p.epi.Z = c.Z; p.epi.Y = c.Y;
+  p.epi.act = (int)c.act; p.epi.z_dtype = (int)c.x_dtype; p.epi.y_dtype = (int)c.y_dtype;
+  p.ksw = plan.ksw; p.nblk = plan.nblk;
+  const cudaError_t e = w4::launch_fused_gemv(p, c.gated, c.x_dtype == W4_BF16, plan.grid, s);
+  if (e != cudaSuccess) return cuda_fail(e, "fused decode launch");
+  return W4_OK;
+}
+
 w4_status fused_run(const FusedCall &c, w4_stream_t stream) {
   t_last_error.clear();
   const w4_status st = fused_check(c);
@@ -196,6 +234,9 @@ w4_status fused_run(const FusedCall &c, w4_stream_t stream) {
   int sm = 0;
   cudaError_t e = current_sm_count(&sm);
   if (e != cudaSuccess) return cuda_fail(e, "device query");
+  GemvFusedPlan gv;
+  if (!c.grad && fused_gemv_plan(c.M, c.N, c.K, c.group, c.gated, sm, gv))
+    return fused_run_gemv(c, gv, reinterpret_cast<cudaStream_t>(stream));
   FusedPlan plan;
   fused_plan(c.M, c.N, c.K, c.gated, c.grad, sm, plan);
   return fused_run_tc(c, plan, reinterpret_cast<cudaStream_t>(stream));

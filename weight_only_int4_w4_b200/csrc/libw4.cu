@@ -25,6 +25,7 @@
 #include "gptq.cu"
 #include "fused_stage.cu"
 #include "fused_tc.cu"
+#include "fused_gemv.cu"
 #include "w4.h"
 
 namespace w4 {

@@ -356,7 +356,6 @@ def w4_awq_search(W: torch.Tensor, Xcal: torch.Tensor, alphas=AWQ_EXPONENTS, gro
 
 # ---------------------------------------------------------------- fused operators
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}  # w4_act of include/w4.h
-_COUNTER_BYTES = 128 * 1024  # the part of a workspace that is zero before and after every call
 
 
 def w4a16_linear_workspace_size(M: int, N: int, K: int) -> int:
@@ -375,89 +374,90 @@ def w4a16_gated_grad_workspace_size(M: int, F: int, K: int) -> int:
     return int(_lib.w4a16_gated_grad_workspace_size(M, F, K))
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+_fused_ws: dict = {}
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_X_DT = {torch.float16: W4_F16, torch.bfloat16: W4_BF16}
 
 
-def _fused_workspace(need: int, dev, raw_stream: int, stream):
-    """Scratch for one fused call on this stream: cached per device and stream, like
-    workspace(); while the stream is being captured into a graph, a buffer of the graph's
-    own (its counters are zeroed by the graph), so that no two graphs share one."""
-    if need == 0:
-        return None
-    capturing = torch.cuda.is_current_stream_capturing()
-    key = (dev, raw_stream)
-    buf = None if capturing else _fused_ws.get(key)
-    if buf is None or buf.numel() < need:
-        with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev):
+def _fused_workspace(need: int, dev, raw: int, stream):
+    """Scratch of a fused call: cached per device and stream, like workspace(); while the stream
+    is being captured into a graph, a buffer of the graph's own, so that no two graphs and
+    no later call share one."""
+    with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev):
+        capturing = torch.cuda.is_current_stream_capturing()
+        buf = None if capturing else _fused_ws.get((dev, raw))
+        if buf is None or buf.numel() < need:
             buf = torch.empty(max(need, 1 << 20), dtype=torch.uint8, device=dev)
-            buf[:_COUNTER_BYTES].zero_()
-        if not capturing:
-            _fused_ws[key] = buf
+            if not capturing:
+                _fused_ws[(dev, raw)] = buf
     return buf
 
 
-_fused_ws: dict = {}
+def _bad(name, what):
+    raise ValueError(f"{name}: {what}")
 
 
-def _fused(name, X, out_cols, packed, scales, zeros, awq_s, group, act, out, out_dtype, ws, stream, extra):
-    """Checks what every fused call has in common, and makes it.  `extra(M, N, K)` gives the
-    call's own tensors (after checking them): the arguments between awq_s and out, and
-    those after out's type."""
-    _need(X.is_cuda and X.dim() == 2 and X.is_contiguous() and X.dtype in (torch.float16, torch.bfloat16),
-          f"{name}: the activations or gradients are a contiguous 2-D CUDA tensor in fp16 or bf16")
-    _need(packed.dim() == 2 and packed.dtype == torch.uint8 and packed.is_contiguous(), f"{name}: packed is uint8 [N, K/2]")
-    _need(act in ACTS, f"{name}: act is one of {sorted(ACTS)}")
-    _need(isinstance(group, int) and group > 0, f"{name}: group is a positive number")
-    M, dev = X.shape[0], X.device
-    N, K = packed.shape[0], packed.shape[1] * 2
-    for t, what in ((scales, "scales"), (zeros, "zeros")):
-        _need(t.dtype == torch.float16 and t.shape == (N, K // group) and t.is_contiguous(),
-              f"{name}: {what} is fp16 [N, K/group]")
-    if awq_s is not None:
-        _need(awq_s.dtype == torch.float32 and awq_s.shape == (K,) and awq_s.is_contiguous(), f"{name}: awq_s is fp32 [K]")
-    cols = out_cols(N, K)
-    if out is None:
-        out = torch.empty((M, cols), dtype=X.dtype if out_dtype is None else out_dtype, device=dev)
-    else:
-        _need(out.shape == (M, cols) and out.is_contiguous() and out_dtype in (None, out.dtype),
-              f"{name}: out is a contiguous [{M}, {cols}] tensor")
-    _need(out.dtype in _DT, f"{name}: output in fp32, fp16 or bf16")
-    mid, after, given = extra(M, N, K, out.dtype)
-    for t in (packed, scales, zeros, awq_s, out, ws, *given):
-        _need(t is None or t.device == dev, f"{name}: all tensors are on {dev}")
-    _need(ws is None or (ws.dtype == torch.uint8 and ws.is_contiguous()), f"{name}: ws is a contiguous uint8 tensor")
-    if torch.cuda.current_device() != dev.index:
-        with torch.cuda.device(dev):
-            return _fused_call(name, X, M, N, K, group, packed, scales, zeros, awq_s, mid, out, after, ws, stream)
-    return _fused_call(name, X, M, N, K, group, packed, scales, zeros, awq_s, mid, out, after, ws, stream)
-
-
-def _fused_call(name, X, M, N, K, group, packed, scales, zeros, awq_s, mid, out, after, ws, stream):
+def _fused_layer(name, X, packed, scales, zeros, awq_s, group):
+    """The checks that every fused call shares; returns (device, M, N, K)."""
+    if not (X.is_cuda and X.dim() == 2 and X.dtype in _X_DT and X.is_contiguous()):
+        _bad(name, "the activations or gradients are a contiguous 2-D CUDA tensor in fp16 or bf16")
     dev = X.device
-    raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
-    rows = N // 2 if "gated" in name else N
-    if ws is None:
-        ws = _fused_workspace(getattr(_lib, name + "_workspace_size")(M, rows, K), dev, raw, stream)
-    _check(getattr(_lib, name)(X.data_ptr(), _DT[X.dtype], M, rows, K, group, packed.data_ptr(), scales.data_ptr(),
-                               zeros.data_ptr(), 0 if awq_s is None else awq_s.data_ptr(), *mid, out.data_ptr(),
-                               _DT[out.dtype], *after, 0 if ws is None else ws.data_ptr(),
-                               0 if ws is None else ws.numel(), raw), name)
+    if not (packed.dtype == torch.uint8 and packed.dim() == 2 and packed.is_contiguous() and packed.device == dev):
+        _bad(name, "packed is a contiguous uint8 [N, K/2] tensor on the activations' device")
+    if type(group) is not int or group < 1:
+        _bad(name, "group is a positive number")
+    N, K = packed.shape
+    K *= 2
+    shape = (N, K // group)
+    if not (scales.dtype == zeros.dtype == torch.float16 and scales.shape == zeros.shape == shape and
+            scales.is_contiguous() and zeros.is_contiguous() and scales.device == zeros.device == dev):
+        _bad(name, f"scales and zeros are contiguous fp16 tensors of shape {shape} on {dev}")
+    if awq_s is not None:
+        _vector(name, "awq_s", awq_s, K, dev)
+    return dev, X.shape[0], N, K
+
+
+def _vector(name, what, t, n, dev):
+    if not (t.dtype == torch.float32 and t.shape == (n,) and t.is_contiguous() and t.device == dev):
+        _bad(name, f"{what} is a contiguous fp32 tensor of {n} elements on {dev}")
+
+
+def _matrix(name, what, t, M, N, dtype, dev):
+    if not (t.dtype == dtype and t.shape == (M, N) and t.is_contiguous() and t.device == dev):
+        _bad(name, f"{what} is a contiguous {dtype} tensor of shape [{M}, {N}] on {dev}")
+
+
+def _output(name, out, M, N, out_dtype, like):
+    if out is None:
+        if out_dtype is not None and out_dtype not in _DT:
+            _bad(name, "the output is fp32, fp16 or bf16")
+        return like.new_empty((M, N), dtype=out_dtype)
+    if out.dtype not in _DT or out_dtype not in (None, out.dtype):
+        _bad(name, "out is fp32, fp16 or bf16, and of out_dtype if that is given")
+    _matrix(name, "out", out, M, N, out.dtype, like.device)
     return out
 
 
-def _opt(t):
-    return 0 if t is None else t.data_ptr()
+def _act(name, act):
+    a = ACTS.get(act)
+    return a if a is not None else _bad(name, f"act is one of {sorted(ACTS)}")
 
 
-def _check_vec(name, what, t, n):
-    _need(t is None or (t.dtype == torch.float32 and t.shape == (n,) and t.is_contiguous()), f"{name}: {what} is fp32 [{n}]")
-
-
-def _check_mat(name, what, t, shape, dtype):
-    _need(t is None or (t.dtype == dtype and t.shape == shape and t.is_contiguous()),
-          f"{name}: {what} is a contiguous {dtype} tensor of shape {shape}")
+def _fused_call(name, fn, size_fn, sizes, dev, ws, stream, args):
+    """Makes the C call on `dev`: args and then the workspace and stream."""
+    idx = dev.index
+    if torch._C._cuda_getDevice() != idx:
+        with torch.cuda.device(dev):
+            return _fused_call(name, fn, size_fn, sizes, dev, ws, stream, args)
+    raw = _raw_stream(idx) if stream is None else stream.cuda_stream
+    if ws is None:
+        need = size_fn(*sizes)
+        ws = _fused_workspace(need, dev, raw, stream) if need else None
+    elif not (ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev):
+        _bad(name, f"ws is a contiguous uint8 tensor on {dev}")
+    st = fn(*args, ws.data_ptr() if ws is not None else 0, ws.numel() if ws is not None else 0, raw)
+    if st != W4_OK:
+        raise W4Error(st, name)
 
 
 def w4a16_linear(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
@@ -466,20 +466,24 @@ def w4a16_linear(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, ze
                  save_preact: bool = False, group: int = GROUP, ws: torch.Tensor | None = None, stream=None):
     """Y = act(X . W^T + bias) + residual.  X [M,K] fp16/bf16 (CUDA), bias fp32 [N], residual [M,N] of
     the output's type (`out` may be the residual itself); Y in out_dtype (X's type by default).
-    With save_preact, returns (Y, Z), Z = X . W^T + bias in X's type, for w4a16_linear_grad."""
-    Z = None
-
-    def extra(M, N, K, odt):
-        nonlocal Z
-        _need(X.shape[1] == K, f"w4a16_linear: X has {X.shape[1]} channels, the weights {K}")
-        _check_vec("w4a16_linear", "bias", bias, N)
-        _check_mat("w4a16_linear", "residual", residual, (M, N), odt)
-        if save_preact:
-            Z = torch.empty((M, N), dtype=X.dtype, device=X.device)
-        return (_opt(bias), ACTS[act], _opt(residual), _opt(Z)), (), (bias, residual)
-
-    Y = _fused("w4a16_linear", X, lambda N, K: N, packed, scales, zeros, awq_s, group, act, out, out_dtype, ws, stream,
-               extra)
+    With save_preact, returns (Y, Z), Z = X . W^T + bias in X's type, for w4a16_linear_grad.
+    Tensors that do not fit raise ValueError, what the library refuses raises W4Error."""
+    name = "w4a16_linear"
+    dev, M, N, K = _fused_layer(name, X, packed, scales, zeros, awq_s, group)
+    if X.shape[1] != K:
+        _bad(name, f"X has {X.shape[1]} channels, the weights {K}")
+    a = _act(name, act)
+    if bias is not None:
+        _vector(name, "bias", bias, N, dev)
+    Y = _output(name, out, M, N, out_dtype, X)
+    if residual is not None:
+        _matrix(name, "residual", residual, M, N, Y.dtype, dev)
+    Z = X.new_empty((M, N)) if save_preact else None
+    _fused_call(name, _lib.w4a16_linear, _lib.w4a16_linear_workspace_size, (M, N, K), dev, ws, stream,
+                (X.data_ptr(), _X_DT[X.dtype], M, N, K, group, packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(),
+                 0 if awq_s is None else awq_s.data_ptr(), 0 if bias is None else bias.data_ptr(), a,
+                 0 if residual is None else residual.data_ptr(), 0 if Z is None else Z.data_ptr(), Y.data_ptr(),
+                 _DT[Y.dtype]))
     return (Y, Z) if save_preact else Y
 
 
@@ -489,20 +493,23 @@ def w4a16_gated(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zer
                 ws: torch.Tensor | None = None, stream=None):
     """H = act(G) * U with [G U] = X . W^T + bias; the weights' rows are F gate rows, then F up rows.
     H [M,F] in out_dtype (X's type by default).  With save_preact, returns (H, Z), Z = [G U]
-    [M,2F] in X's type, for w4a16_gated_grad."""
-    Z = None
-
-    def extra(M, N, K, odt):
-        nonlocal Z
-        _need(N % 2 == 0, "w4a16_gated: the weights have an even number of rows, gate rows first")
-        _need(X.shape[1] == K, f"w4a16_gated: X has {X.shape[1]} channels, the weights {K}")
-        _check_vec("w4a16_gated", "bias", bias, N)
-        if save_preact:
-            Z = torch.empty((M, N), dtype=X.dtype, device=X.device)
-        return (_opt(bias), ACTS[act], _opt(Z)), (), (bias,)
-
-    H = _fused("w4a16_gated", X, lambda N, K: N // 2, packed, scales, zeros, awq_s, group, act, out, out_dtype, ws,
-               stream, extra)
+    [M,2F] in X's type, for w4a16_gated_grad.  Errors as w4a16_linear."""
+    name = "w4a16_gated"
+    dev, M, N, K = _fused_layer(name, X, packed, scales, zeros, awq_s, group)
+    if X.shape[1] != K:
+        _bad(name, f"X has {X.shape[1]} channels, the weights {K}")
+    if N % 2:
+        _bad(name, "the weights have an even number of rows, gate rows first")
+    a = _act(name, act)
+    if bias is not None:
+        _vector(name, "bias", bias, N, dev)
+    F = N // 2
+    H = _output(name, out, M, F, out_dtype, X)
+    Z = X.new_empty((M, N)) if save_preact else None
+    _fused_call(name, _lib.w4a16_gated, _lib.w4a16_gated_workspace_size, (M, F, K), dev, ws, stream,
+                (X.data_ptr(), _X_DT[X.dtype], M, F, K, group, packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(),
+                 0 if awq_s is None else awq_s.data_ptr(), 0 if bias is None else bias.data_ptr(), a,
+                 0 if Z is None else Z.data_ptr(), H.data_ptr(), _DT[H.dtype]))
     return (H, Z) if save_preact else H
 
 
@@ -511,9 +518,10 @@ def w4a16_linear_grad(dY: torch.Tensor, packed: torch.Tensor, scales: torch.Tens
                       dbias: bool = False, out_dtype=None, out: torch.Tensor | None = None, group: int = GROUP,
                       ws: torch.Tensor | None = None, stream=None):
     """dX [M,K] = (dY * act'(Z)) . W^ for frozen weights.  dY [M,N] fp16/bf16 (CUDA), preact = Z [M,N] of
-    its type (not needed for act "none").  With dbias, returns (dX, dbias fp32 [N])."""
-    return _grad("w4a16_linear_grad", dY, lambda N: N, packed, scales, zeros, awq_s, preact, act, dbias, out_dtype,
-                 out, group, ws, stream)
+    its type (not needed for act "none").  With dbias, returns (dX, dbias fp32 [N]).  Errors as
+    w4a16_linear."""
+    return _grad("w4a16_linear_grad", False, _lib.w4a16_linear_grad, _lib.w4a16_linear_grad_workspace_size, dY, packed,
+                 scales, zeros, awq_s, preact, act, dbias, out_dtype, out, group, ws, stream)
 
 
 def w4a16_gated_grad(dH: torch.Tensor, preact: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
@@ -521,24 +529,28 @@ def w4a16_gated_grad(dH: torch.Tensor, preact: torch.Tensor, packed: torch.Tenso
                      out_dtype=None, out: torch.Tensor | None = None, group: int = GROUP,
                      ws: torch.Tensor | None = None, stream=None):
     """dX [M,K] = [dG dU] . W^ with dG = dH * U * act'(G), dU = dH * act(G), from preact = [G U] [M,2F] of
-    dH's type.  With dbias, returns (dX, dbias fp32 [2F])."""
-    return _grad("w4a16_gated_grad", dH, lambda N: N // 2, packed, scales, zeros, awq_s, preact, act, dbias, out_dtype,
-                 out, group, ws, stream)
+    dH's type.  With dbias, returns (dX, dbias fp32 [2F]).  Errors as w4a16_linear."""
+    return _grad("w4a16_gated_grad", True, _lib.w4a16_gated_grad, _lib.w4a16_gated_grad_workspace_size, dH, packed,
+                 scales, zeros, awq_s, preact, act, dbias, out_dtype, out, group, ws, stream)
 
 
-def _grad(name, dY, width, packed, scales, zeros, awq_s, preact, act, dbias, out_dtype, out, group, ws, stream):
-    db = None
-
-    def extra(M, N, K, odt):
-        nonlocal db
-        _need(N % 2 == 0 or name != "w4a16_gated_grad", f"{name}: the weights have an even number of rows, gate rows first")
-        _need(dY.shape[1] == width(N), f"{name}: the gradient has {dY.shape[1]} channels, the weights give {width(N)}")
-        _check_mat(name, "preact", preact, (M, N), dY.dtype)
-        if dbias:
-            db = torch.empty(N, dtype=torch.float32, device=dY.device)
-        return (_opt(preact), ACTS[act]), (_opt(db),), (preact,)
-
-    dX = _fused(name, dY, lambda N, K: K, packed, scales, zeros, awq_s, group, act, out, out_dtype, ws, stream, extra)
+def _grad(name, gated, fn, size_fn, dY, packed, scales, zeros, awq_s, preact, act, dbias, out_dtype, out, group, ws,
+          stream):
+    dev, M, N, K = _fused_layer(name, dY, packed, scales, zeros, awq_s, group)
+    if gated and N % 2:
+        _bad(name, "the weights have an even number of rows, gate rows first")
+    width = N // 2 if gated else N
+    if dY.shape[1] != width:
+        _bad(name, f"the gradient has {dY.shape[1]} channels, the weights give {width}")
+    a = _act(name, act)
+    if preact is not None:
+        _matrix(name, "preact", preact, M, N, dY.dtype, dev)
+    dX = _output(name, out, M, K, out_dtype, dY)
+    db = dY.new_empty(N, dtype=torch.float32) if dbias else None
+    _fused_call(name, fn, size_fn, (M, width, K), dev, ws, stream,
+                (dY.data_ptr(), _X_DT[dY.dtype], M, width, K, group, packed.data_ptr(), scales.data_ptr(),
+                 zeros.data_ptr(), 0 if awq_s is None else awq_s.data_ptr(), 0 if preact is None else preact.data_ptr(),
+                 a, dX.data_ptr(), _DT[dX.dtype], 0 if db is None else db.data_ptr()))
     return (dX, db) if dbias else dX
 
 
