@@ -75,23 +75,34 @@ bool fused_plan(int64_t M, int64_t N, int64_t K, bool gated, bool grad, int sm, 
 }
 
 // Up to 16 tokens on groups of 128: one kernel, no workspace.  Splits K over as many of a
-// CTA's 16 warps as there are pieces of channels and room for the partial sums; CTAs are
-// as many as SMs, or a multiple where their rows' partial sums would not fit.
+// CTA's 16 warps as there are pieces of channels and room for the partial sums; ranges of
+// rows are as many as SMs (or clusters), or a multiple where the partial sums of one would
+// not fit.  Clusters of 2 or 4 where a CTA's activations would be over a quarter of its
+// weights (2 M K bytes against N K / 2 / SMs).
 struct GemvFusedPlan {
-  int grid = 0, ksw = 1, nblk = 1;
+  int grid = 0, ksw = 1, nblk = 1, cluster = 1, depth = 3;
 };
 bool fused_gemv_plan(int64_t M, int64_t N, int64_t K, int group, bool gated, int sm, GemvFusedPlan &p) {
   if (group != w4::kGroup || M > w4::fgv::kMaxTokens) return false;
+  if ((double)N * (double)(K / w4::kGroup) > 4.0e9) return false;  // groups are numbered in 32 bits
   const int64_t out = gated ? N / 2 : N, pieces = cdiv(K / w4::kGroup, M <= 8 ? 2 : 1);
-  for (int64_t grid = std::min<int64_t>(sm, cdiv(out, 8)); grid <= (int64_t)1 << 20; grid *= 2) {
-    const int64_t nblk = cdiv(cdiv(out, grid), 16) * (gated ? 2 : 1);
-    for (int ksw = 16; ksw >= 1; ksw /= 2) {
-      if (ksw > pieces || w4::fgv::smem_bytes(ksw, 1, (int)M) * nblk > w4::fgv::kSmemMax) continue;
-      p.grid = (int)grid;
-      p.ksw = ksw;
-      p.nblk = (int)nblk;
-      return true;
-    }
+  int cluster = 1;
+  while (cluster < 4 && 2.0 * M / cluster > 0.125 * (double)N / sm && pieces >= 4 * cluster) cluster *= 2;
+  const int64_t most = w4::fused_gemv_clusters(cluster, sm);
+  for (int64_t ranges = std::min<int64_t>(most, cdiv(out, 8)); ranges <= (int64_t)1 << 20; ranges *= 2) {
+    const int64_t nblk = cdiv(cdiv(out, ranges), 16) * (gated ? 2 : 1);
+    for (int ksw = 16; ksw >= 1; ksw /= 2)
+      for (int depth = 4; depth >= 3; --depth) {
+        if (ksw * cluster > pieces ||
+            w4::fgv::smem_bytes(ksw, (int)std::min<int64_t>(nblk, 1 << 16), (int)M, cluster, depth) > w4::fgv::kSmemMax)
+          continue;
+        p.grid = (int)ranges * cluster;
+        p.ksw = ksw;
+        p.nblk = (int)nblk;
+        p.cluster = cluster;
+        p.depth = depth;
+        return true;
+      }
   }
   return false;
 }
@@ -151,10 +162,8 @@ w4_status fused_check(const FusedCall &c) {
   for (int i = 0; i < 8; ++i)
     if (overlap(c.workspace, c.workspace_bytes, ins[i].p, ins[i].n))
       return fail(W4_ERR_INVALID_ARG, "the workspace overlaps an input");
-  GemvFusedPlan gv;
-  const size_t need = !c.grad && fused_gemv_plan(c.M, c.N, c.K, c.group, c.gated, sm_count_or_b200(), gv)
-                          ? 0
-                          : fused_ws_bytes(c.M, c.N, c.K, c.gated, c.grad);
+  const bool decode = !c.grad && c.group == w4::kGroup && c.M <= w4::fgv::kMaxTokens;
+  const size_t need = decode ? 0 : plan.bytes;
   if (need > 0 && (!c.workspace || c.workspace_bytes < need))
     return fail(W4_ERR_INVALID_ARG, "workspace too small: need %zu bytes, got %zu", need,
                 c.workspace ? c.workspace_bytes : (size_t)0);
@@ -215,14 +224,24 @@ w4_status fused_run_tc(const FusedCall &c, const FusedPlan &plan, cudaStream_t s
 }
 
 w4_status fused_run_gemv(const FusedCall &c, const GemvFusedPlan &plan, cudaStream_t s) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+  if (!enc) return fail(W4_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const bool two = w4::fgv::groups((int)c.M) == 2;
+  CUtensorMap tmP;
+  const CUresult r = encode_2d(enc, &tmP, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.packed, (uint64_t)(c.K / 2), (uint64_t)c.N,
+                               (uint64_t)(c.K / 2), two ? 128u : 64u, 16u,
+                               two ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+  if (r != CUDA_SUCCESS) return fail(W4_ERR_CUDA, "tensor map for packed weights failed (CUresult %d)", (int)r);
   w4::FusedGemvParams p{};
   p.X = static_cast<const uint16_t *>(c.X);
   p.M = c.M; p.N = c.gated ? c.N / 2 : c.N; p.K = c.K;
   p.packed = c.packed; p.scales = c.scales; p.zeros = c.zeros; p.awq_s = c.awq_s;
   p.epi.bias = c.bias; p.epi.residual = c.residual; p.epi.Z = c.Z; p.epi.Y = c.Y;
   p.epi.act = (int)c.act; p.epi.z_dtype = (int)c.x_dtype; p.epi.y_dtype = (int)c.y_dtype;
-  p.ksw = plan.ksw; p.nblk = plan.nblk;
-  const cudaError_t e = w4::launch_fused_gemv(p, c.gated, c.x_dtype == W4_BF16, plan.grid, s);
+  p.depth = plan.depth;
+  p.ksw = plan.ksw; p.nblk = plan.nblk; p.cluster = plan.cluster;
+  const cudaError_t e = w4::launch_fused_gemv(tmP, p, c.gated, c.x_dtype == W4_BF16, plan.grid, s);
   if (e != cudaSuccess) return cuda_fail(e, "fused decode launch");
   return W4_OK;
 }
@@ -235,8 +254,11 @@ w4_status fused_run(const FusedCall &c, w4_stream_t stream) {
   cudaError_t e = current_sm_count(&sm);
   if (e != cudaSuccess) return cuda_fail(e, "device query");
   GemvFusedPlan gv;
-  if (!c.grad && fused_gemv_plan(c.M, c.N, c.K, c.group, c.gated, sm, gv))
+  if (!c.grad && c.group == w4::kGroup && c.M <= w4::fgv::kMaxTokens) {
+    if (!fused_gemv_plan(c.M, c.N, c.K, c.group, c.gated, sm, gv))
+      return fail(W4_ERR_INVALID_ARG, "N=%lld K=%lld: too many groups for one launch", (long long)c.N, (long long)c.K);
     return fused_run_gemv(c, gv, reinterpret_cast<cudaStream_t>(stream));
+  }
   FusedPlan plan;
   fused_plan(c.M, c.N, c.K, c.gated, c.grad, sm, plan);
   return fused_run_tc(c, plan, reinterpret_cast<cudaStream_t>(stream));

@@ -376,6 +376,7 @@ def w4a16_gated_grad_workspace_size(M: int, F: int, K: int) -> int:
 
 _fused_ws: dict = {}
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_DECODE_TOKENS = 16  # up to here, with groups of 128, a forward call needs no workspace
 _X_DT = {torch.float16: W4_F16, torch.bfloat16: W4_BF16}
 
 
@@ -383,13 +384,15 @@ def _fused_workspace(need: int, dev, raw: int, stream):
     """Scratch of a fused call: cached per device and stream, like workspace(); while the stream
     is being captured into a graph, a buffer of the graph's own, so that no two graphs and
     no later call share one."""
-    with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev):
-        capturing = torch.cuda.is_current_stream_capturing()
-        buf = None if capturing else _fused_ws.get((dev, raw))
-        if buf is None or buf.numel() < need:
-            buf = torch.empty(max(need, 1 << 20), dtype=torch.uint8, device=dev)
-            if not capturing:
-                _fused_ws[(dev, raw)] = buf
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _fused_workspace(need, dev, raw, None)
+    capturing = torch.cuda.is_current_stream_capturing()
+    buf = None if capturing else _fused_ws.get((dev, raw))
+    if buf is None or buf.numel() < need:
+        buf = torch.empty(max(need, 1 << 20), dtype=torch.uint8, device=dev)
+        if not capturing:
+            _fused_ws[(dev, raw)] = buf
     return buf
 
 
@@ -451,8 +454,9 @@ def _fused_call(name, fn, size_fn, sizes, dev, ws, stream, args):
             return _fused_call(name, fn, size_fn, sizes, dev, ws, stream, args)
     raw = _raw_stream(idx) if stream is None else stream.cuda_stream
     if ws is None:
-        need = size_fn(*sizes)
-        ws = _fused_workspace(need, dev, raw, stream) if need else None
+        if size_fn is not None:
+            need = size_fn(*sizes)
+            ws = _fused_workspace(need, dev, raw, stream) if need else None
     elif not (ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev):
         _bad(name, f"ws is a contiguous uint8 tensor on {dev}")
     st = fn(*args, ws.data_ptr() if ws is not None else 0, ws.numel() if ws is not None else 0, raw)
@@ -479,7 +483,8 @@ def w4a16_linear(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, ze
     if residual is not None:
         _matrix(name, "residual", residual, M, N, Y.dtype, dev)
     Z = X.new_empty((M, N)) if save_preact else None
-    _fused_call(name, _lib.w4a16_linear, _lib.w4a16_linear_workspace_size, (M, N, K), dev, ws, stream,
+    decode = M <= _DECODE_TOKENS and group == GROUP
+    _fused_call(name, _lib.w4a16_linear, None if decode else _lib.w4a16_linear_workspace_size, (M, N, K), dev, ws, stream,
                 (X.data_ptr(), _X_DT[X.dtype], M, N, K, group, packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(),
                  0 if awq_s is None else awq_s.data_ptr(), 0 if bias is None else bias.data_ptr(), a,
                  0 if residual is None else residual.data_ptr(), 0 if Z is None else Z.data_ptr(), Y.data_ptr(),
@@ -506,7 +511,8 @@ def w4a16_gated(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zer
     F = N // 2
     H = _output(name, out, M, F, out_dtype, X)
     Z = X.new_empty((M, N)) if save_preact else None
-    _fused_call(name, _lib.w4a16_gated, _lib.w4a16_gated_workspace_size, (M, F, K), dev, ws, stream,
+    decode = M <= _DECODE_TOKENS and group == GROUP
+    _fused_call(name, _lib.w4a16_gated, None if decode else _lib.w4a16_gated_workspace_size, (M, F, K), dev, ws, stream,
                 (X.data_ptr(), _X_DT[X.dtype], M, F, K, group, packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(),
                  0 if awq_s is None else awq_s.data_ptr(), 0 if bias is None else bias.data_ptr(), a,
                  0 if Z is None else Z.data_ptr(), H.data_ptr(), _DT[H.dtype]))
