@@ -37,7 +37,7 @@ __device__ __forceinline__ void act_both(float x, int act, float &y, float &dy) 
     case kActSilu: {
       const float s = logistic(x);
       y = x * s;
-      dy = s + y * logistic(-x);  // s (1 + x (1 - s)), 1 - s = logistic(-x)
+      dy = s + y * (1.0f - s);  // s (1 + x (1 - s)): off by an ulp of x where s is near 1
       break;
     }
     case kActGelu: {
@@ -50,7 +50,7 @@ __device__ __forceinline__ void act_both(float x, int act, float &y, float &dy) 
       const float v = 2.0f * kSqrt2OverPi * (x + kGeluCubic * x * x * x);
       const float s = logistic(v);
       y = x * s;
-      dy = s + y * logistic(-v) * 2.0f * kSqrt2OverPi * (1.0f + 3.0f * kGeluCubic * x * x);
+      dy = s + y * (1.0f - s) * 2.0f * kSqrt2OverPi * (1.0f + 3.0f * kGeluCubic * x * x);
       break;
     }
     default:

@@ -68,13 +68,12 @@ bool fused_plan(int64_t M, int64_t N, int64_t K, bool gated, bool grad, int sm, 
   p.tab = p.rinv + align256((size_t)N * 4);
   p.part = p.tab + align256((size_t)N * (K / 32) * 4);  // room for groups of 32
   p.dbias = p.part + align256((size_t)2 * p.tail_ctas * p.bn * 128 * 4);
-  const size_t db = !grad ? 0
-                          : (size_t)std::max(w4::fused_dbias_ranges(M, N, true), w4::fused_dbias_ranges(M, N, false)) * N * 4;
+  const size_t db = !grad ? 0 : (size_t)w4::fused_dbias_parts(M, N, gated, sm) * N * 4;
   p.bytes = p.dbias + align256(db);
   return true;
 }
 
-// Up to 16 tokens on groups of 128: one kernel, no workspace.  Splits K over as many of a
+// Up to 8 tokens on groups of 128: one kernel, no workspace.  Splits K over as many of a
 // CTA's 16 warps as there are pieces of channels and room for the partial sums; ranges of
 // rows are as many as SMs (or clusters), or a multiple where the partial sums of one would
 // not fit.  Clusters of 2 or 4 where a CTA's activations would be over a quarter of its
@@ -85,7 +84,7 @@ struct GemvFusedPlan {
 bool fused_gemv_plan(int64_t M, int64_t N, int64_t K, int group, bool gated, int sm, GemvFusedPlan &p) {
   if (group != w4::kGroup || M > w4::fgv::kMaxTokens) return false;
   if ((double)N * (double)(K / w4::kGroup) > 4.0e9) return false;  // groups are numbered in 32 bits
-  const int64_t out = gated ? N / 2 : N, pieces = cdiv(K / w4::kGroup, M <= 8 ? 2 : 1);
+  const int64_t out = gated ? N / 2 : N, pieces = cdiv(K / w4::kGroup, 2);
   int cluster = 1;
   while (cluster < 4 && 2.0 * M / cluster > 0.125 * (double)N / sm && pieces >= 4 * cluster) cluster *= 2;
   const int64_t most = w4::fused_gemv_clusters(cluster, sm);
@@ -107,6 +106,41 @@ bool fused_gemv_plan(int64_t M, int64_t N, int64_t K, int group, bool gated, int
   return false;
 }
 
+// 9 to 64 tokens on groups of 128, on the tensor cores.  For 1, 2, 4 or 8 CTAs to a range of
+// rows, the cycles of a CTA: its (tile, group) pairs, each the larger of what the bytes of
+// a tile's rows take at an SM's share of HBM and what their conversion takes.
+struct SkinnyFusedPlan {
+  int grid = 0, cluster = 1, tiles = 1, tile_rows = 0, bn = 16;
+  size_t xp = 0, tinv = 0, bytes = 0;
+};
+bool fused_skinny_plan(int64_t M, int64_t N, int64_t K, int group, bool gated, int sm, SkinnyFusedPlan &p) {
+  if (group != w4::kGroup || K % w4::kGroup != 0 || M > w4::fsk::kMaxTokens) return false;
+  constexpr double kConvert = 300.0, kBytesPerCycle = 23.4, kCluster = 2000.0;
+  const int64_t out = gated ? N / 2 : N, Kg = K / w4::kGroup, lim = gated ? 64 : 128;
+  p.bn = (int)(cdiv(M, 16) * 16);
+  double best = 0;
+  for (int cluster = 1; cluster <= 8 && cluster <= Kg; cluster *= 2) {
+    const int64_t ranges = std::min<int64_t>(w4::fused_gemv_clusters(cluster, sm), cdiv(out, 8));
+    const int64_t rows = cdiv(out, ranges), tiles = cdiv(rows, lim), tile_rows = cdiv(rows, tiles);
+    if (tiles > 1 << 20 || tiles * cdiv(Kg, cluster) > 1 << 30 ||
+        w4::fsk::code_stages(p.bn, (int)M, (int)std::min<int64_t>(tiles, 512), cluster) < 3)
+      continue;
+    const double unit = std::max(kConvert, (double)tile_rows * (gated ? 2 : 1) * 68.0 / kBytesPerCycle);
+    const double cost = (double)tiles * (double)cdiv(Kg, cluster) * unit + (cluster > 1 ? kCluster : 0.0);
+    if (p.grid == 0 || cost < best) {
+      best = cost;
+      p.grid = (int)ranges * cluster;
+      p.cluster = cluster;
+      p.tiles = (int)tiles;
+      p.tile_rows = (int)tile_rows;
+    }
+  }
+  p.xp = kCounterBytes;
+  p.tinv = p.xp + align256((size_t)K * p.bn * 2);
+  p.bytes = p.tinv + align256((size_t)p.bn * 4);
+  return p.grid > 0;
+}
+
 int sm_count_or_b200() {
   int sm = 0;
   return current_sm_count(&sm) == cudaSuccess ? sm : 148;
@@ -114,7 +148,21 @@ int sm_count_or_b200() {
 
 size_t fused_ws_bytes(int64_t M, int64_t N, int64_t K, bool gated, bool grad) {
   FusedPlan p;
-  return fused_plan(M, N, K, gated, grad, sm_count_or_b200(), p) ? p.bytes : 0;
+  const int sm = sm_count_or_b200();
+  if (!fused_plan(M, N, K, gated, grad, sm, p)) return 0;
+  SkinnyFusedPlan sp;
+  if (!grad && fused_skinny_plan(M, N, K, w4::kGroup, gated, sm, sp)) return std::max(p.bytes, sp.bytes);
+  return p.bytes;
+}
+
+// Which kernel serves a call.  Measured on B200 at the 8B and 70B layer shapes, microseconds of
+// decode / small-batch kernel: 8 tokens 9.4 / 12 (4096 x 4096), 19 / 23 (14336 -> 4096), 25 /
+// 30 (4096 -> 2 x 14336), 72 / 97 (8192 -> 2 x 28672); 16 tokens 14 / 12, 28 / 23, 43 / 30,
+// 128 / 97.  Small-batch / prefill kernel at 64 tokens: 15 / 25, 27 / 41, 36 / 51, 110 / 140.
+enum FusedRoute { kRouteDecode, kRouteSkinny, kRouteTc };
+FusedRoute fused_route(const FusedCall &c) {
+  if (c.grad || c.group != w4::kGroup || c.M > w4::fsk::kMaxTokens) return kRouteTc;
+  return c.M <= w4::fgv::kMaxTokens ? kRouteDecode : kRouteSkinny;
 }
 
 // Everything a fused call can be refused for, checked on the host.
@@ -162,8 +210,7 @@ w4_status fused_check(const FusedCall &c) {
   for (int i = 0; i < 8; ++i)
     if (overlap(c.workspace, c.workspace_bytes, ins[i].p, ins[i].n))
       return fail(W4_ERR_INVALID_ARG, "the workspace overlaps an input");
-  const bool decode = !c.grad && c.group == w4::kGroup && c.M <= w4::fgv::kMaxTokens;
-  const size_t need = decode ? 0 : plan.bytes;
+  const size_t need = fused_route(c) == kRouteDecode ? 0 : fused_ws_bytes(c.M, c.N, c.K, c.gated, c.grad);
   if (need > 0 && (!c.workspace || c.workspace_bytes < need))
     return fail(W4_ERR_INVALID_ARG, "workspace too small: need %zu bytes, got %zu", need,
                 c.workspace ? c.workspace_bytes : (size_t)0);
@@ -171,7 +218,7 @@ w4_status fused_check(const FusedCall &c) {
 }
 
 // The tensor-core path: operand staging, the product, and the sum of cut tiles.
-w4_status fused_run_tc(const FusedCall &c, const FusedPlan &plan, cudaStream_t s) {
+w4_status fused_run_tc(const FusedCall &c, const FusedPlan &plan, int sm, cudaStream_t s) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   if (!enc) return fail(W4_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   uint8_t *ws = static_cast<uint8_t *>(c.workspace);
@@ -190,13 +237,9 @@ w4_status fused_run_tc(const FusedCall &c, const FusedPlan &plan, cudaStream_t s
   if (r != CUDA_SUCCESS) return fail(W4_ERR_CUDA, "tensor map for packed weights failed (CUresult %d)", (int)r);
   cudaError_t e;
   if (c.grad) {
-    if (c.dbias) {
-      e = w4::launch_fused_dbias(c.X, c.Z, (int)c.x_dtype, (int)c.act, c.gated, c.M, c.N,
-                                 reinterpret_cast<float *>(ws + plan.dbias), c.dbias, s);
-      if (e != cudaSuccess) return cuda_fail(e, "bias gradient launch");
-    }
     e = w4::launch_fused_stage_dz(c.X, c.act == W4_ACT_NONE && !c.gated ? nullptr : c.Z, (int)c.x_dtype, (int)c.act,
-                                  c.gated, c.M, c.N, plan.ld, c.scales, c.zeros, kg, xp, tinv, rinv, tab, s);
+                                  c.gated, c.M, c.N, plan.ld, c.scales, c.zeros, kg, xp, tinv, rinv, tab,
+                                  reinterpret_cast<float *>(ws + plan.dbias), c.dbias, sm, s);
   } else {
     e = w4::launch_fused_stage_x(c.X, c.x_dtype == W4_BF16, c.awq_s, c.M, c.K, c.scales, c.zeros, kg, c.N, xp, tinv, rinv,
                                  tab, s);
@@ -211,7 +254,7 @@ w4_status fused_run_tc(const FusedCall &c, const FusedPlan &plan, cudaStream_t s
   p.epi.residual = c.residual; p.epi.Z = c.grad ? nullptr : c.Z; p.epi.Y = c.Y;
   p.epi.act = c.grad ? (int)W4_ACT_NONE : (int)c.act;
   p.epi.z_dtype = (int)c.x_dtype; p.epi.y_dtype = (int)c.y_dtype;
-  p.epi.vec = p.epi.N % 8 == 0;
+  p.epi.vec = p.epi.N % 4 == 0;
   p.tab = tab;
   p.rows = c.N; p.kg = kg;
   p.gshift = c.group == 128 ? 7 : c.group == 64 ? 6 : 5;
@@ -220,18 +263,48 @@ w4_status fused_run_tc(const FusedCall &c, const FusedPlan &plan, cudaStream_t s
   p.part = reinterpret_cast<float *>(ws + plan.part);
   e = w4::launch_fused_tc(c.grad ? w4::kGrad : c.gated ? w4::kGated : w4::kLinear, tmX, tmP, p, plan.grid, s);
   if (e != cudaSuccess) return cuda_fail(e, "fused product launch");
+  if (c.dbias) {
+    e = w4::launch_fused_dbias_sum(c.M, c.N, c.gated, reinterpret_cast<const float *>(ws + plan.dbias), c.dbias, sm, s);
+    if (e != cudaSuccess) return cuda_fail(e, "bias gradient launch");
+  }
+  return W4_OK;
+}
+
+w4_status fused_run_skinny(const FusedCall &c, const SkinnyFusedPlan &plan, cudaStream_t s) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+  if (!enc) return fail(W4_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  uint8_t *ws = static_cast<uint8_t *>(c.workspace);
+  uint16_t *xp = reinterpret_cast<uint16_t *>(ws + plan.xp);
+  float *tinv = reinterpret_cast<float *>(ws + plan.tinv);
+  CUtensorMap tmX, tmP;
+  CUresult r = encode_2d(enc, &tmX, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xp, 64u, (uint64_t)(c.K / 64) * plan.bn, 128u, 64u,
+                         2u * plan.bn, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+  if (r != CUDA_SUCCESS) return fail(W4_ERR_CUDA, "tensor map for staged activations failed (CUresult %d)", (int)r);
+  r = encode_2d(enc, &tmP, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.packed, (uint64_t)(c.K / 2), (uint64_t)c.N,
+                (uint64_t)(c.K / 2), 128u, (uint32_t)plan.tile_rows, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+  if (r != CUDA_SUCCESS) return fail(W4_ERR_CUDA, "tensor map for packed weights failed (CUresult %d)", (int)r);
+  cudaError_t e = w4::launch_fused_stage_small(c.X, c.x_dtype == W4_BF16, c.awq_s, c.M, c.K, plan.bn, xp, tinv, s);
+  if (e != cudaSuccess) return cuda_fail(e, "activation staging launch");
+  w4::FusedSkinnyParams p{};
+  p.epi.M = c.M; p.epi.N = c.gated ? c.N / 2 : c.N;
+  p.epi.tinv = tinv; p.epi.bias = c.bias; p.epi.residual = c.residual; p.epi.Z = c.Z; p.epi.Y = c.Y;
+  p.epi.act = (int)c.act; p.epi.z_dtype = (int)c.x_dtype; p.epi.y_dtype = (int)c.y_dtype;
+  p.scales = c.scales; p.zeros = c.zeros;
+  p.groups = (int)(c.K / w4::kGroup);
+  p.tile_rows = plan.tile_rows; p.tiles = plan.tiles; p.cluster = plan.cluster;
+  p.code_stages = w4::fsk::code_stages(plan.bn, (int)c.M, plan.tiles, plan.cluster);
+  e = w4::launch_fused_skinny(tmX, tmP, p, c.gated, plan.grid, s);
+  if (e != cudaSuccess) return cuda_fail(e, "fused small-batch launch");
   return W4_OK;
 }
 
 w4_status fused_run_gemv(const FusedCall &c, const GemvFusedPlan &plan, cudaStream_t s) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   if (!enc) return fail(W4_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  const bool two = w4::fgv::groups((int)c.M) == 2;
   CUtensorMap tmP;
   const CUresult r = encode_2d(enc, &tmP, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.packed, (uint64_t)(c.K / 2), (uint64_t)c.N,
-                               (uint64_t)(c.K / 2), two ? 128u : 64u, 16u,
-                               two ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+                               (uint64_t)(c.K / 2), 128u, 16u, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
   if (r != CUDA_SUCCESS) return fail(W4_ERR_CUDA, "tensor map for packed weights failed (CUresult %d)", (int)r);
   w4::FusedGemvParams p{};
   p.X = static_cast<const uint16_t *>(c.X);
@@ -253,15 +326,20 @@ w4_status fused_run(const FusedCall &c, w4_stream_t stream) {
   int sm = 0;
   cudaError_t e = current_sm_count(&sm);
   if (e != cudaSuccess) return cuda_fail(e, "device query");
-  GemvFusedPlan gv;
-  if (!c.grad && c.group == w4::kGroup && c.M <= w4::fgv::kMaxTokens) {
+  const FusedRoute route = fused_route(c);
+  if (route == kRouteDecode) {
+    GemvFusedPlan gv;
     if (!fused_gemv_plan(c.M, c.N, c.K, c.group, c.gated, sm, gv))
       return fail(W4_ERR_INVALID_ARG, "N=%lld K=%lld: too many groups for one launch", (long long)c.N, (long long)c.K);
     return fused_run_gemv(c, gv, reinterpret_cast<cudaStream_t>(stream));
   }
+  SkinnyFusedPlan sk;
+  // (not where the tiles of a range pass what one CTA counts: the prefill kernel then)
+  if (route == kRouteSkinny && fused_skinny_plan(c.M, c.N, c.K, c.group, c.gated, sm, sk))
+    return fused_run_skinny(c, sk, reinterpret_cast<cudaStream_t>(stream));
   FusedPlan plan;
   fused_plan(c.M, c.N, c.K, c.gated, c.grad, sm, plan);
-  return fused_run_tc(c, plan, reinterpret_cast<cudaStream_t>(stream));
+  return fused_run_tc(c, plan, sm, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t fused_ws_query(int64_t M, int64_t N, int64_t K, bool gated, bool grad) {

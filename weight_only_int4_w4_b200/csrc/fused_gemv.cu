@@ -1,4 +1,4 @@
-// fused_gemv.cu -- w4a16_linear and w4a16_gated for up to 16 tokens (groups of 128), in one
+// fused_gemv.cu -- w4a16_linear and w4a16_gated for up to 8 tokens (groups of 128), in one
 // kernel without workspace: the call reads every weight once and is bound by that.
 //
 // A CTA (one per SM) owns an equal range of output rows, whatever its length, so that
@@ -50,14 +50,15 @@ struct FusedGemvParams {
 namespace fgv {
 
 constexpr int kWarps = 16;
-constexpr int kMaxTokens = 16;
+constexpr int kMaxTokens = 8;
 constexpr int kSmemMax = 226 * 1024;
 
-__host__ __device__ constexpr int groups(int m) { return m <= 8 ? 2 : 1; }  // groups per piece
+constexpr int C = 2;              // groups per piece
+constexpr int kPiece = C * 1024;  // 16 rows of them
 // the warps' rings, their barriers, partial sums per warp, and a cluster's sums per CTA
-__host__ __device__ constexpr int ring_bytes(int depth, int m) { return kWarps * depth * (groups(m) * 1024 + 8) + 1024; }
+__host__ __device__ constexpr int ring_bytes(int depth) { return kWarps * depth * (kPiece + 8) + 1024; }
 __host__ __device__ constexpr int smem_bytes(int ksw, int nblk, int m, int cluster, int depth) {
-  return ring_bytes(depth, m) + (ksw + (cluster > 1 ? 1 : 0)) * nblk * 16 * ((m + 1) & ~1) * 4;
+  return ring_bytes(depth) + (ksw + (cluster > 1 ? 1 : 0)) * nblk * 16 * ((m + 1) & ~1) * 4;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -117,8 +118,10 @@ __device__ __forceinline__ uint32_t ldg_u32(const uint16_t *p) {
 
 // The activations of 32 channels of `C` groups (token row x, channels ch + 128 c ..; nothing
 // where !in) as B fragments, and the factor 2^-b.  Lanes of a token (t = 0..3) share b.
-template <bool kBf16, int C>
-__device__ __forceinline__ float stage_b(const uint16_t *x, const float *awq_s, bool in, int last, uint32_t (&bf)[C][16]) {
+template <bool kBf16>
+__device__ __forceinline__ float stage_b(const uint16_t *x, const float *awq_s, bool in, int last,
+                                         uint32_t (&bf)[fgv::C][16]) {
+  using fgv::C;
   uint4 raw[C][4];
   uint32_t top = 0;
 #pragma unroll
@@ -184,13 +187,9 @@ __device__ __forceinline__ float stage_b(const uint16_t *x, const float *awq_s, 
   return e.y;
 }
 
-// T octets of tokens; C groups per piece (C = 2 for one octet, so that its B fragments, 32
-// registers, and two pieces of weights in flight fit 128 registers; C = 1 for two octets).
-template <int T, bool kGated, bool kBf16>
+template <bool kGated, bool kBf16>
 __global__ void __launch_bounds__(fgv::kWarps * 32, 1) fused_gemv_kernel(const __grid_constant__ CUtensorMap tmP, const FusedGemvParams p) {
   using namespace fgv;
-  constexpr int C = T == 1 ? 2 : 1;
-  constexpr int kPiece = C * 1024;  // 16 rows of C groups
   extern __shared__ uint8_t gemv_smem[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(gemv_smem) + 1023) & ~uintptr_t(1023));
   const int depth = p.depth;
@@ -251,10 +250,7 @@ __global__ void __launch_bounds__(fgv::kWarps * 32, 1) fused_gemv_kernel(const _
     for (int h = 0; h < 2; ++h) {
       uint32_t r = (uint32_t)((g + 8 * h) * Kg);
       if (in + 15 > last) r = (uint32_t)(min(g + 8 * h, last - in) * Kg);  // the range ends in this block
-      if (C == 1) {
-        sz[h][0] = ldg_u16(sp + r);
-        sz[h][1] = ldg_u16(zp + r);
-      } else if (even) {
+      if (even) {
         sz[h][0] = ldg_u32(sp + r);
         sz[h][1] = ldg_u32(zp + r);
       } else {
@@ -269,101 +265,90 @@ __global__ void __launch_bounds__(fgv::kWarps * 32, 1) fused_gemv_kernel(const _
     if (i < total) load(i);
   if (total > 0) load_sz(rs, c0);
 
-  uint32_t bf[T][C][16];           // B fragments
-  float d1[T][C][2], inv[T][2];    // D1 and 2^-b of tokens 2t, 2t + 1
+  uint32_t bf[C][16];        // B fragments
+  float d1[C][2], inv[2];    // D1 and 2^-b of tokens 2t, 2t + 1
   int blk = rs, cc = c0, slot = 0;
   uint32_t ph = 0;
   bool ok = true;
   float *dst = sPart + ((size_t)(kw * p.nblk + blk) * 16 + g) * Mp + 2 * t;
   const int step = rsets * 16 * Mp;
   for (int it = 0; it < total; ++it) {
-      if (blk == rs) {
-        // a new piece of channels
+    if (blk == rs) {
+      // a new piece of channels
+      const int64_t ch = (int64_t)cc * C * kGroup + 32 * t;
+      const float v = stage_b<kBf16>(p.X + (int64_t)g * p.K + ch, p.awq_s ? p.awq_s + ch : nullptr, g < M,
+                                     Kg - 1 - C * cc, bf);
+      inv[0] = __shfl_sync(~0u, v, 8 * t);
+      inv[1] = __shfl_sync(~0u, v, 8 * t + 4);
+      constexpr uint32_t one[4] = {0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u};
 #pragma unroll
-        for (int o = 0; o < T; ++o) {
-          const int64_t ch = (int64_t)cc * C * kGroup + 32 * t;
-          const float v = stage_b<kBf16, C>(p.X + (int64_t)(8 * o + g) * p.K + ch, p.awq_s ? p.awq_s + ch : nullptr,
-                                            8 * o + g < M, Kg - 1 - C * cc, bf[o]);
-          inv[o][0] = __shfl_sync(~0u, v, 8 * t);
-          inv[o][1] = __shfl_sync(~0u, v, 8 * t + 4);
-          constexpr uint32_t one[4] = {0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u};
+      for (int c = 0; c < C; ++c) {
+        float d[4];
 #pragma unroll
-          for (int c = 0; c < C; ++c) {
-            float d[4];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) mma(d, one, bf[o][c][2 * q], bf[o][c][2 * q + 1], q == 0);
-            d1[o][c][0] = d[0];
-            d1[o][c][1] = d[1];
-          }
-        }
+        for (int q = 0; q < 8; ++q) mma(d, one, bf[c][2 * q], bf[c][2 * q + 1], q == 0);
+        d1[c][0] = d[0];
+        d1[c][1] = d[1];
       }
-      if (!ftc::wait_all(&bar[slot], ph, kErrTimeoutTma)) { ok = false; break; }
-      uint4 w[C][2];
-      const uint32_t at = smem_u32(ring + slot * kPiece) + g * (C * 64);  // row g + 8 has the same swizzle
+    }
+    if (!ftc::wait_all(&bar[slot], ph, kErrTimeoutTma)) { ok = false; break; }
+    uint4 w[C][2];
+    const uint32_t at = smem_u32(ring + slot * kPiece) + g * (C * 64);  // row g + 8 has the same swizzle
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-          w[c][h] = lds128_ordered(at + h * (8 * C * 64) + ((uint32_t)((4 * c + t) ^ (C == 2 ? g : g >> 1)) << 4));
-      float d[C][T][4], y[T][4];
+      for (int c = 0; c < C; ++c)
+        w[c][h] = lds128_ordered(at + h * (8 * C * 64) + ((uint32_t)((4 * c + t) ^ g) << 4));
+    float d[C][4], y[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const uint4 u = w[c][0], v = w[c][1];
-          const uint32_t l = q == 0 ? u.x : q == 1 ? u.y : q == 2 ? u.z : u.w, l8 = l >> 8;
-          const uint32_t x = q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w, x8 = x >> 8;
-          const uint32_t a0[4] = {l & 0x000F000Fu, x & 0x000F000Fu, l & 0x00F000F0u, x & 0x00F000F0u};
-          const uint32_t a1[4] = {l8 & 0x000F000Fu, x8 & 0x000F000Fu, l8 & 0x00F000F0u, x8 & 0x00F000F0u};
+      for (int c = 0; c < C; ++c) {
+        const uint4 u = w[c][0], v = w[c][1];
+        const uint32_t l = q == 0 ? u.x : q == 1 ? u.y : q == 2 ? u.z : u.w, l8 = l >> 8;
+        const uint32_t x = q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w, x8 = x >> 8;
+        const uint32_t a0[4] = {l & 0x000F000Fu, x & 0x000F000Fu, l & 0x00F000F0u, x & 0x00F000F0u};
+        const uint32_t a1[4] = {l8 & 0x000F000Fu, x8 & 0x000F000Fu, l8 & 0x00F000F0u, x8 & 0x00F000F0u};
+        mma(d[c], a0, bf[c][4 * q], bf[c][4 * q + 1], q == 0);
+        mma(d[c], a1, bf[c][4 * q + 2], bf[c][4 * q + 3], false);
+      }
+    // sums in units of 2^24, which the epilogue puts back
 #pragma unroll
-          for (int o = 0; o < T; ++o) {
-            mma(d[c][o], a0, bf[o][c][4 * q], bf[o][c][4 * q + 1], q == 0);
-            mma(d[c][o], a1, bf[o][c][4 * q + 2], bf[o][c][4 * q + 3], false);
-          }
-        }
-      // sums in units of 2^24, which the epilogue puts back
+    for (int h = 0; h < 2; ++h) {
+      const __half2 sc = *reinterpret_cast<const __half2 *>(&sz[h][0]), zp = *reinterpret_cast<const __half2 *>(&sz[h][1]);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float v = __low2float(sc) * fmaf(-__low2float(zp), d1[0][x], d[0][2 * h + x]);
+        y[2 * h + x] = fmaf(__high2float(sc), fmaf(-__high2float(zp), d1[1][x], d[1][2 * h + x]), v) * inv[x];
+      }
+    }
+    // the slot was read (its values went through the MMAs above): refill it, and fetch the
+    // next piece's constants
+    if (it + depth < total) load(slot);
+    if (++slot == depth) slot = 0, ph ^= 1u;
+    {
+      const bool turn = blk + rsets >= nb;
+      if (it + 1 < total) load_sz(turn ? rs : blk + rsets, turn ? cc + p.ksw : cc);
+    }
+    if (2 * t < M) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const __half2 sc = *reinterpret_cast<const __half2 *>(&sz[h][0]), zp = *reinterpret_cast<const __half2 *>(&sz[h][1]);
-#pragma unroll
-        for (int o = 0; o < T; ++o)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float v = __low2float(sc) * fmaf(-__low2float(zp), d1[o][0][x], d[0][o][2 * h + x]);
-            if constexpr (C == 2) v = fmaf(__high2float(sc), fmaf(-__high2float(zp), d1[o][1][x], d[1][o][2 * h + x]), v);
-            y[o][2 * h + x] = v * inv[o][x];
-          }
-      }
-      // the slot was read (its values went through the MMAs above): refill it, and fetch the
-      // next piece's constants
-      if (it + depth < total) load(slot);
-      if (++slot == depth) slot = 0, ph ^= 1u;
-      {
-        const bool turn = blk + rsets >= nb;
-        if (it + 1 < total) load_sz(turn ? rs : blk + rsets, turn ? cc + p.ksw : cc);
-      }
-#pragma unroll
-      for (int o = 0; o < T; ++o)
-        if (8 * o + 2 * t < M) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float2 *q = reinterpret_cast<float2 *>(dst + 8 * h * Mp + 8 * o);
-            float2 v = make_float2(y[o][2 * h], y[o][2 * h + 1]);
-            if (cc != c0) {
-              const float2 u = *q;
-              v.x += u.x;
-              v.y += u.y;
-            }
-            *q = v;
-          }
+        float2 *q = reinterpret_cast<float2 *>(dst + 8 * h * Mp);
+        float2 v = make_float2(y[2 * h], y[2 * h + 1]);
+        if (cc != c0) {
+          const float2 u = *q;
+          v.x += u.x;
+          v.y += u.y;
         }
-      blk += rsets;
-      dst += step;
-      if (blk >= nb) {
-        blk = rs;
-        cc += p.ksw;
-        dst = sPart + ((size_t)(kw * p.nblk + blk) * 16 + g) * Mp + 2 * t;
+        *q = v;
       }
+    }
+    blk += rsets;
+    dst += step;
+    if (blk >= nb) {
+      blk = rs;
+      cc += p.ksw;
+      dst = sPart + ((size_t)(kw * p.nblk + blk) * 16 + g) * Mp + 2 * t;
+    }
   }
   if (!ok) {  // a wait that ran out: give copies in flight time to land
     const uint64_t t0 = globaltimer_ns();
@@ -422,7 +407,7 @@ int fused_gemv_clusters(int cluster, int sm) {
   if (cluster == 1) return sm;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kAttrDevices) return sm / cluster;
-  std::atomic<int> &k = known[dev][cluster == 2 ? 0 : 1];
+  std::atomic<int> &k = known[dev][cluster == 2 ? 0 : cluster == 4 ? 1 : 2];
   int n = k.load(std::memory_order_relaxed);
   if (n == 0) {
     cudaLaunchConfig_t cfg = {};
@@ -434,7 +419,7 @@ int fused_gemv_clusters(int cluster, int sm) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, fused_gemv_kernel<1, false, true>, &cfg) != cudaSuccess || n < 1) {
+    if (cudaOccupancyMaxActiveClusters(&n, fused_gemv_kernel<false, true>, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();
       n = sm / cluster;
     }
@@ -443,12 +428,12 @@ int fused_gemv_clusters(int cluster, int sm) {
   return n;
 }
 
-template <int T, bool kGated, bool kBf16>
+template <bool kGated, bool kBf16>
 cudaError_t launch_fused_gemv_t(const CUtensorMap &tmP, const FusedGemvParams &p, int grid, cudaStream_t s) {
   static std::atomic<int> attr[kAttrDevices];
   const int smem = fgv::smem_bytes(p.ksw, p.nblk, (int)p.M, p.cluster, p.depth);
   if (smem > 48 * 1024) {
-    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(fused_gemv_kernel<T, kGated, kBf16>), smem, attr);
+    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(fused_gemv_kernel<kGated, kBf16>), smem, attr);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -464,15 +449,12 @@ cudaError_t launch_fused_gemv_t(const CUtensorMap &tmP, const FusedGemvParams &p
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = p.cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, fused_gemv_kernel<T, kGated, kBf16>, tmP, p);
+  return cudaLaunchKernelEx(&cfg, fused_gemv_kernel<kGated, kBf16>, tmP, p);
 }
 
 cudaError_t launch_fused_gemv(const CUtensorMap &tmP, const FusedGemvParams &p, bool gated, bool bf16, int grid, cudaStream_t s) {
-  if (p.M <= 8)
-    return gated ? (bf16 ? launch_fused_gemv_t<1, true, true>(tmP, p, grid, s) : launch_fused_gemv_t<1, true, false>(tmP, p, grid, s))
-                 : (bf16 ? launch_fused_gemv_t<1, false, true>(tmP, p, grid, s) : launch_fused_gemv_t<1, false, false>(tmP, p, grid, s));
-  return gated ? (bf16 ? launch_fused_gemv_t<2, true, true>(tmP, p, grid, s) : launch_fused_gemv_t<2, true, false>(tmP, p, grid, s))
-               : (bf16 ? launch_fused_gemv_t<2, false, true>(tmP, p, grid, s) : launch_fused_gemv_t<2, false, false>(tmP, p, grid, s));
+  return gated ? (bf16 ? launch_fused_gemv_t<true, true>(tmP, p, grid, s) : launch_fused_gemv_t<true, false>(tmP, p, grid, s))
+               : (bf16 ? launch_fused_gemv_t<false, true>(tmP, p, grid, s) : launch_fused_gemv_t<false, false>(tmP, p, grid, s));
 }
 
 }  // namespace w4

@@ -199,11 +199,142 @@ __device__ __forceinline__ void dz_at(const void *dY, const void *Z, int dtype, 
   }
 }
 
-// dz' = fp16(dZ / r[n] * e) of one token per block, natural order, columns N.. up to the
-// row stride `ld` zero, and 1 / e.  Two passes: the second finds its inputs in L2.
+// dz' = fp16(dZ / r[n] * e), natural order, and 1 / e.  A cluster of CTAs takes tokens in turn,
+// each CTA the same 512 kDzVecs outputs f (of a gated call: rows f and F + f, which share
+// their inputs) of every token: dZ stays in registers while the CTAs exchange the token's
+// largest value, the next token's inputs are on their way meanwhile, and dbias's sums
+// over the cluster's tokens, to part [cluster][N], cost nothing but additions.
+constexpr int kDzThreads = 256, kDzVecs = 2, kDzSlice = kDzThreads * kDzVecs * 8;
+
+template <bool kGated, bool kBias>
+__global__ void __launch_bounds__(kDzThreads, 2)
+    fused_stage_dz(const uint16_t *dY, const uint16_t *Z, int bf16, int act, int64_t M, int64_t N, const float *rinv,
+                   uint16_t *dzp, float *tinv, float *part) {
+  constexpr int R = kGated ? 2 : 1;
+  __shared__ __align__(16) float srinv[R][kDzSlice];
+  __shared__ float red[kDzThreads / 32];
+  __shared__ float peers[2][8];
+  const int slices = gridDim.x, slice = blockIdx.x;  // a cluster is a row of the grid
+  const int64_t F = kGated ? N / 2 : N;
+  grid_launch_dependents();
+  grid_dependency_wait();  // the row factors
+  int64_t f[kDzVecs];
+#pragma unroll
+  for (int i = 0; i < kDzVecs; ++i) f[i] = ((int64_t)slice * kDzVecs * kDzThreads + i * kDzThreads + threadIdx.x) * 8;
+  for (int j = threadIdx.x; j < kDzSlice; j += kDzThreads) {
+    const int64_t n = (int64_t)slice * kDzSlice + j;
+#pragma unroll
+    for (int h = 0; h < R; ++h) srinv[h][j] = n < F ? rinv[h * F + n] : 0.0f;
+  }
+  __syncthreads();
+  if (slices > 1)  // every CTA of the cluster runs before one writes to another
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  uint4 raw[kDzVecs][1 + R];  // dY; Z (gated: G, U)
+  auto fetch = [&](int64_t m) {
+#pragma unroll
+    for (int i = 0; i < kDzVecs; ++i) {
+      const bool in = m < M && f[i] < F;
+      raw[i][0] = in ? *reinterpret_cast<const uint4 *>(dY + m * F + f[i]) : make_uint4(0, 0, 0, 0);
+      raw[i][1] = in && Z ? *reinterpret_cast<const uint4 *>(Z + m * N + f[i]) : make_uint4(0, 0, 0, 0);
+      if constexpr (kGated) raw[i][2] = in ? *reinterpret_cast<const uint4 *>(Z + m * N + F + f[i]) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  auto widen = [&](const uint4 &w, float (&v)[8]) {
+    if (bf16) unpack8<true>(w, v);
+    else unpack8<false>(w, v);
+  };
+  float acc[kBias ? kDzVecs : 1][R][8] = {};
+  fetch(blockIdx.y);
+  int par = 0;
+  for (int64_t m = blockIdx.y; m < M; m += gridDim.y, par ^= 1) {
+    float d[kDzVecs][R][8];
+    float mx = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kDzVecs; ++i) {
+      float g[8], a[8], u[8];
+      widen(raw[i][0], g);
+      widen(raw[i][1], a);
+      if constexpr (kGated) widen(raw[i][R], u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float y = 0.0f, s = 1.0f;
+        if (Z) act_both(a[j], act, y, s);
+        if constexpr (kGated) {
+          d[i][0][j] = g[j] * u[j] * s;
+          d[i][R - 1][j] = g[j] * y;
+        } else {
+          d[i][0][j] = g[j] * s;
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < R; ++h) {
+        const float *q = srinv[h] + (i * kDzThreads + threadIdx.x) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+          const float4 x = *reinterpret_cast<const float4 *>(q + j);
+          const float r4[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (kBias) acc[i][h][j + k] += d[i][h][j + k];
+            d[i][h][j + k] *= r4[k];
+            mx = fmaxf(mx, fabsf(d[i][h][j + k]));
+          }
+        }
+      }
+    }
+    fetch(m + gridDim.y);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mx;
+    __syncthreads();
+    mx = red[0];
+#pragma unroll
+    for (int i = 1; i < kDzThreads / 32; ++i) mx = fmaxf(mx, red[i]);
+    if (slices > 1) {
+      if (threadIdx.x < slices) {  // this CTA's largest value to every CTA of the cluster
+        uint32_t to;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(&peers[par][slice])), "r"(threadIdx.x));
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(mx) : "memory");
+      }
+      asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+      for (int i = 0; i < slices; ++i) mx = fmaxf(mx, peers[par][i]);
+    } else {
+      __syncthreads();  // red is read until here
+    }
+    const float2 e = pow2_to(mx, 13);
+    if (slice == 0 && threadIdx.x == 0) tinv[m] = e.y;
+#pragma unroll
+    for (int i = 0; i < kDzVecs; ++i)
+      if (f[i] < F)
+#pragma unroll
+        for (int h = 0; h < R; ++h) {
+          const float(&x)[8] = d[i][h];
+          *reinterpret_cast<uint4 *>(dzp + m * N + h * F + f[i]) =
+              make_uint4(half2_bits(x[0] * e.x, x[1] * e.x), half2_bits(x[2] * e.x, x[3] * e.x),
+                         half2_bits(x[4] * e.x, x[5] * e.x), half2_bits(x[6] * e.x, x[7] * e.x));
+        }
+  }
+  if constexpr (kBias) {
+#pragma unroll
+    for (int i = 0; i < kDzVecs; ++i)
+      if (f[i] < F)
+#pragma unroll
+        for (int h = 0; h < R; ++h) {
+          float4 *o = reinterpret_cast<float4 *>(part + (int64_t)blockIdx.y * N + h * F + f[i]);
+          o[0] = make_float4(acc[i][h][0], acc[i][h][1], acc[i][h][2], acc[i][h][3]);
+          o[1] = make_float4(acc[i][h][4], acc[i][h][5], acc[i][h][6], acc[i][h][7]);
+        }
+  }
+  if (slices > 1)  // no CTA leaves while another may write to it
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The same for rows that do not start on 16 bytes or are longer than a cluster's slices: one
+// token per block, in two passes (the second finds its inputs in L2); columns N.. up to
+// the row stride `ld` become 0.
 template <bool kGated, int kVec>
 __global__ void __launch_bounds__(512)
-    fused_stage_dz(const void *dY, const void *Z, int dtype, int act, int64_t N, int64_t ld, const float *rinv,
+    fused_stage_dz_rows(const void *dY, const void *Z, int dtype, int act, int64_t N, int64_t ld, const float *rinv,
                    uint16_t *dzp, float *tinv) {
   grid_launch_dependents();
   grid_dependency_wait();  // the row factors
@@ -267,6 +398,7 @@ __global__ void __launch_bounds__(256) fused_dbias_sum(const float *part, int ra
   const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (n >= N) return;
   float s = 0.0f;
+#pragma unroll 8
   for (int i = 0; i < ranges; ++i) s += part[i * N + n];
   dbias[n] = s;
 }
@@ -298,39 +430,73 @@ cudaError_t launch_fused_stage_x(const void *X, bool bf16, const float *awq_s, i
   return cudaGetLastError();
 }
 
-cudaError_t launch_fused_stage_dz(const void *dY, const void *Z, int dtype, int act, bool gated, int64_t M, int64_t N,
-                                  int64_t ld, const uint16_t *scales, const uint16_t *zeros, int64_t kg, uint16_t *dzp,
-                                  float *tinv, float *rinv, uint32_t *tab, cudaStream_t s) {
-  fused_prep<<<(unsigned)((N + kPrepRows - 1) / kPrepRows), kStageThreads, 0, s>>>(scales, zeros, kg, N, rinv, tab);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // 16-byte vectors where every row (and its gated half) starts on one
-  const bool vec = (gated ? N / 2 : N) % 8 == 0;
-  auto k = gated ? (vec ? fused_stage_dz<true, 8> : fused_stage_dz<true, 1>)
-                 : (vec ? fused_stage_dz<false, 8> : fused_stage_dz<false, 1>);
-  return launch_pdl(k, dim3((unsigned)M), dim3(512), 0, s, dY, Z, dtype, act, N, ld, (const float *)rinv, dzp, tinv);
+// Whether dz' is staged by clusters that hold a token between them.
+bool fused_dz_clusters(int64_t N, bool gated) {
+  const int64_t F = gated ? N / 2 : N;
+  return F % 8 == 0 && F <= 8 * kDzSlice;
 }
-
-// Token ranges of dbias: about four blocks per SM, at least 8 tokens each.
-int64_t fused_dbias_ranges(int64_t M, int64_t N, bool vec) {
+// Its clusters: two CTAs per SM, at most one per token.
+int64_t fused_dz_grid(int64_t M, int64_t N, bool gated, int sm) {
+  const int64_t F = gated ? N / 2 : N, slices = (F + kDzSlice - 1) / kDzSlice, n = 2 * (int64_t)sm / slices;
+  return M < n ? M : n < 1 ? 1 : n;
+}
+// Rows of dbias's partial sums: clusters, or ranges of tokens (about four blocks per SM, at
+// least 8 tokens each).
+int64_t fused_dbias_parts(int64_t M, int64_t N, bool gated, int sm) {
+  if (fused_dz_clusters(N, gated)) return fused_dz_grid(M, N, gated, sm);
+  const bool vec = (gated ? N / 2 : N) % 8 == 0;
   const int64_t cols = (N + (vec ? 256 : 32) - 1) / (vec ? 256 : 32);
   int64_t r = (600 + cols - 1) / cols;
   r = r > (M + 7) / 8 ? (M + 7) / 8 : r;
   return r < 1 ? 1 : r;
 }
 
-cudaError_t launch_fused_dbias(const void *dY, const void *Z, int dtype, int act, bool gated, int64_t M, int64_t N,
-                               float *part, float *dbias, cudaStream_t s) {
-  const bool vec = (gated ? N / 2 : N) % 8 == 0;
-  int64_t ranges = fused_dbias_ranges(M, N, vec);
-  const int64_t per = (M + ranges - 1) / ranges;
-  ranges = (M + per - 1) / per;
-  const dim3 grid((unsigned)((N + (vec ? 256 : 32) - 1) / (vec ? 256 : 32)), (unsigned)ranges);
-  float *to = ranges == 1 ? dbias : part;
-  auto k = gated ? (vec ? fused_dbias_part<true, 8> : fused_dbias_part<true, 1>)
-                 : (vec ? fused_dbias_part<false, 8> : fused_dbias_part<false, 1>);
-  k<<<grid, 256, 0, s>>>(dY, Z, dtype, act, M, N, per, to);
-  if (ranges > 1) fused_dbias_sum<<<(unsigned)((N + 255) / 256), 256, 0, s>>>(part, (int)ranges, N, dbias);
+cudaError_t launch_fused_stage_dz(const void *dY, const void *Z, int dtype, int act, bool gated, int64_t M, int64_t N,
+                                  int64_t ld, const uint16_t *scales, const uint16_t *zeros, int64_t kg, uint16_t *dzp,
+                                  float *tinv, float *rinv, uint32_t *tab, float *part, float *dbias, int sm,
+                                  cudaStream_t s) {
+  const bool vec = (gated ? N / 2 : N) % 8 == 0, clusters = fused_dz_clusters(N, gated);
+  int64_t parts = dbias ? fused_dbias_parts(M, N, gated, sm) : 0;
+  if (dbias && !clusters) {
+    const int64_t per = (M + parts - 1) / parts;
+    parts = (M + per - 1) / per;
+    const dim3 grid((unsigned)((N + (vec ? 256 : 32) - 1) / (vec ? 256 : 32)), (unsigned)parts);
+    auto k = gated ? (vec ? fused_dbias_part<true, 8> : fused_dbias_part<true, 1>)
+                   : (vec ? fused_dbias_part<false, 8> : fused_dbias_part<false, 1>);
+    k<<<grid, 256, 0, s>>>(dY, Z, dtype, act, M, N, per, part);
+    fused_dbias_sum<<<(unsigned)((N + 255) / 256), 256, 0, s>>>(part, (int)parts, N, dbias);
+  }
+  fused_prep<<<(unsigned)((N + kPrepRows - 1) / kPrepRows), kStageThreads, 0, s>>>(scales, zeros, kg, N, rinv, tab);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  if (!clusters) {
+    auto k = gated ? (vec ? fused_stage_dz_rows<true, 8> : fused_stage_dz_rows<true, 1>)
+                   : (vec ? fused_stage_dz_rows<false, 8> : fused_stage_dz_rows<false, 1>);
+    return launch_pdl(k, dim3((unsigned)M), dim3(512), 0, s, dY, Z, dtype, act, N, ld, (const float *)rinv, dzp, tinv);
+  }
+  const int64_t F = gated ? N / 2 : N;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((F + kDzSlice - 1) / kDzSlice), (unsigned)fused_dz_grid(M, N, gated, sm));
+  cfg.blockDim = dim3(kDzThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cfg.gridDim.x;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cfg.gridDim.x > 1 ? 2 : 1;
+  auto k = gated ? (dbias ? fused_stage_dz<true, true> : fused_stage_dz<true, false>)
+                 : (dbias ? fused_stage_dz<false, true> : fused_stage_dz<false, false>);
+  return cudaLaunchKernelEx(&cfg, k, static_cast<const uint16_t *>(dY), static_cast<const uint16_t *>(Z), dtype == 2 ? 1 : 0,
+                            act, M, N, (const float *)rinv, dzp, tinv, part);
+}
+
+// Behind the product (which does not wait for it): dbias from the clusters' sums.
+cudaError_t launch_fused_dbias_sum(int64_t M, int64_t N, bool gated, const float *part, float *dbias, int sm, cudaStream_t s) {
+  if (!fused_dz_clusters(N, gated)) return cudaSuccess;  // summed already
+  fused_dbias_sum<<<(unsigned)((N + 255) / 256), 256, 0, s>>>(part, (int)fused_dbias_parts(M, N, gated, sm), N, dbias);
   return cudaGetLastError();
 }
 

@@ -44,7 +44,7 @@ struct FusedEpi {
   const float *colmul;      // gradient: awq_s, or NULL
   const void *residual;     // or NULL
   void *Z, *Y;              // Z or NULL
-  int act, z_dtype, y_dtype, vec;  // vec: 8 outputs in a row start on 16 bytes
+  int act, z_dtype, y_dtype, vec;  // vec: N is a multiple of 4
 };
 
 struct FusedTcParams {
@@ -72,7 +72,7 @@ constexpr int kMaxBn = 208;
 constexpr int kMaxActStages = 8;
 
 __host__ __device__ constexpr int fixed_bytes(bool grad) {
-  return 1024 + kCodeStages * kCodeStage + 2 * kStageOut + (grad ? kSets * kGradAStage : 0) + 2 * 256 * 4 + 512;
+  return 1024 + kCodeStages * kCodeStage + 2 * kStageOut + (grad ? kSets * kGradAStage : 0) + 256 * 4 + 512;
 }
 __host__ __device__ inline int act_stages(int bn, bool grad) {
   const int n = (227 * 1024 - fixed_bytes(grad)) / (bn * kAct);
@@ -93,6 +93,18 @@ __device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// Whether the phase is complete, without waiting (try_wait may suspend the thread for
+// microseconds).
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // mbar_wait by a whole warp with one answer, so that the warp-wide instructions behind it
@@ -206,103 +218,93 @@ __device__ __forceinline__ void tile_at(const FusedTcParams &p, int t, int &row,
 // {0,4,1,5,2,6,3,7}[j] of a word at place j.
 __device__ __forceinline__ int grad_row(int r) { return (r & ~7) | ((r & 1) << 2) | ((r >> 1) & 3); }
 
-__device__ __forceinline__ void put8(void *p, int dtype, int64_t i, const float (&v)[8]) {
-  if (dtype == 0) {
-    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
-    o[0] = make_float4(v[0], v[1], v[2], v[3]);
-    o[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else if (dtype == 1) {
-    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) =
-        make_uint4(half2_bits(v[0], v[1]), half2_bits(v[2], v[3]), half2_bits(v[4], v[5]), half2_bits(v[6], v[7]));
+__device__ __forceinline__ void widen4(const uint2 &w, int dtype, float (&v)[4]) {
+  if (dtype == 2) {
+    v[0] = __uint_as_float(w.x << 16);
+    v[1] = __uint_as_float(w.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(w.y << 16);
+    v[3] = __uint_as_float(w.y & 0xFFFF0000u);
   } else {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-      w[j] = *reinterpret_cast<const uint32_t *>(&b);
-    }
-    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&w.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
+    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
   }
-}
-__device__ __forceinline__ void add8(const void *p, int dtype, int64_t i, float (&v)[8]) {
-  float a[8];
-  if (dtype == 0) {
-    const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-    const float4 x = q[0], y = q[1];
-    a[0] = x.x; a[1] = x.y; a[2] = x.z; a[3] = x.w; a[4] = y.x; a[5] = y.y; a[6] = y.z; a[7] = y.w;
-  } else {
-    const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
-    if (dtype == 2) unpack8<true>(w, a);
-    else unpack8<false>(w, a);
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] += a[j];
 }
 
-// Stores v[0..8) at columns n.. of a row that starts at element `row`; n + j < lim.
-__device__ __forceinline__ void put_row(void *p, int dtype, int64_t row, int64_t n, int64_t lim, bool vec,
-                                        const float (&v)[8]) {
-  if (vec && n + 8 <= lim) {
-    put8(p, dtype, row + n, v);
+// Stores v at columns n.. of a row that starts at element `row`; n + j < lim.
+__device__ __forceinline__ void put4(void *p, int dtype, int64_t row, int64_t n, int64_t lim, bool vec, const float (&v)[4]) {
+  if (vec) {  // lim is a multiple of 4
+    if (dtype == 0) {
+      *reinterpret_cast<float4 *>(static_cast<float *>(p) + row + n) = make_float4(v[0], v[1], v[2], v[3]);
+    } else if (dtype == 1) {
+      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + row + n) = make_uint2(half2_bits(v[0], v[1]), half2_bits(v[2], v[3]));
+    } else {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(v[0], v[1]), y = __floats2bfloat162_rn(v[2], v[3]);
+      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + row + n) =
+          make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+    }
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 4; ++j)
       if (n + j < lim) store_from_float(p, dtype, row + n + j, v[j]);
   }
 }
 
-// Factor and bias of eight output columns (0 behind the last).
+// Factor and bias of four output columns (0 behind the last); first: packed row (forward) or
+// channel (gradient) of the first one, column n of lim.
 struct ColK {
-  float f[8], b[8];
-  // first: packed row (forward) or channel (gradient) of column 0
+  float f[4], b[4];
   __device__ __forceinline__ void load(const FusedEpi &e, bool grad, int64_t first, int64_t n, int64_t lim) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4; ++j) {
       const bool ok = n + j < lim;
       f[j] = !ok ? 0.0f : grad ? (e.colmul ? e.colmul[first + j] : 1.0f) : e.rinv[first + j];
       b[j] = ok && e.bias ? e.bias[first + j] : 0.0f;
     }
   }
+  // z = v * factor / e + bias
+  __device__ __forceinline__ void scale(const float4 &v, float inv, float (&z)[4]) const {
+    z[0] = v.x * f[0] * inv + b[0];
+    z[1] = v.y * f[1] * inv + b[1];
+    z[2] = v.z * f[2] * inv + b[2];
+    z[3] = v.w * f[3] * inv + b[3];
+  }
 };
 
-// z = v * factor / e + bias
-__device__ __forceinline__ void scale8(const float (&v)[8], const ColK &c, float inv, float (&z)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) z[j] = v[j] * c.f[j] * inv + c.b[j];
+// The residual's four values at (m, n), as they lie (16 bits, aligned) or nothing.
+__device__ __forceinline__ uint2 residual4(const FusedEpi &e, int64_t m, int64_t n) {
+  return *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(e.residual) + m * e.N + n);
 }
 
-__device__ __forceinline__ void finish_linear(const FusedEpi &e, int64_t m, int64_t n, float (&z)[8]) {
+// `res`: the residual's values where `have`, else they are read here.
+__device__ __forceinline__ void finish_linear(const FusedEpi &e, int64_t m, int64_t n, float (&z)[4], bool have, const uint2 &res) {
   const int64_t row = m * e.N;
-  if (e.Z) put_row(e.Z, e.z_dtype, row, n, e.N, e.vec, z);
+  if (e.Z) put4(e.Z, e.z_dtype, row, n, e.N, e.vec, z);
   if (e.act != kActNone) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) z[j] = act_fwd(z[j], e.act);
+    for (int j = 0; j < 4; ++j) z[j] = act_fwd(z[j], e.act);
   }
-  if (e.residual) {
-    if (e.vec && n + 8 <= e.N) {
-      add8(e.residual, e.y_dtype, row + n, z);
-    } else {
+  if (have) {
+    float a[4];
+    widen4(res, e.y_dtype, a);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (n + j < e.N) z[j] += load_as_float(e.residual, e.y_dtype, row + n + j);
-    }
+    for (int j = 0; j < 4; ++j) z[j] += a[j];
+  } else if (e.residual) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (n + j < e.N) z[j] += load_as_float(e.residual, e.y_dtype, row + n + j);
   }
-  put_row(e.Y, e.y_dtype, row, n, e.N, e.vec, z);
+  put4(e.Y, e.y_dtype, row, n, e.N, e.vec, z);
 }
 
-__device__ __forceinline__ void finish_gated(const FusedEpi &e, int64_t m, int64_t f, float (&g)[8], const float (&u)[8]) {
+__device__ __forceinline__ void finish_gated(const FusedEpi &e, int64_t m, int64_t f, float (&g)[4], const float (&u)[4]) {
   if (e.Z) {
-    put_row(e.Z, e.z_dtype, m * 2 * e.N, f, e.N, e.vec, g);
-    put_row(e.Z, e.z_dtype, m * 2 * e.N + e.N, f, e.N, e.vec, u);
+    put4(e.Z, e.z_dtype, m * 2 * e.N, f, e.N, e.vec, g);
+    put4(e.Z, e.z_dtype, m * 2 * e.N + e.N, f, e.N, e.vec, u);
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) g[j] = act_fwd(g[j], e.act) * u[j];
-  put_row(e.Y, e.y_dtype, m * e.N, f, e.N, e.vec, g);
-}
-
-__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  for (int j = 0; j < 4; ++j) g[j] = act_fwd(g[j], e.act) * u[j];
+  put4(e.Y, e.y_dtype, m * e.N, f, e.N, e.vec, g);
 }
 
 }  // namespace ftc
@@ -419,7 +421,7 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
         const uint64_t bd = smem_desc_k_sw128(smem_u32(sX + s * act_stage));
         uint64_t *done = &empty[s];
         if (++s == ns) s = 0, ph ^= 1u;
-        ready = __all_sync(~0u, mbar_try_wait(&full[s], ph));
+        ready = __all_sync(~0u, mbar_test(&full[s], ph));
         if (elect_one()) {
           if constexpr (kIsGrad) {
             // MN-major A: 64-channel halves 8192 bytes apart (leading offset), 8-row
@@ -556,17 +558,29 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
       tile_at(p, tile, row, tok);
       const int64_t m0 = (int64_t)tok * p.bn;
       for (int t = tid; t < p.bn; t += 128) sTok[t] = m0 + t < e.M ? e.tinv[m0 + t] : 0.0f;
+      // four columns of the tile (gated: and the same of the up half), and with 32 (16)
+      // lanes to a token, a warp's 8 tokens of a chunk of 32
+      constexpr int kLanes = kMode == kGated ? 16 : 32, kTok = 8 * kLanes / 32, kStep = 32 / kLanes;
+      const int col = 4 * (lane & (kLanes - 1)), t0 = 8 * q + lane / kLanes;
+      const int64_t n = (int64_t)row * (kMode == kGated ? 64 : 128) + col;
       ColK c0, c1;
-      const int64_t n = kMode == kGated ? (int64_t)row * 64 + 8 * (tid & 7) : (int64_t)row * 128 + 8 * (tid & 15);
       if (slot < 0) {
         c0.load(e, kIsGrad, n, n, e.N);
         if (kMode == kGated) c1.load(e, false, e.N + n, n, e.N);
       }
+      const bool ahead = kMode == kLinear && slot < 0 && e.residual && e.vec && e.y_dtype != 0 && n < e.N;
       if (!vote_epilogue(mbar_wait(&dfull[d], dph, kErrTimeoutEpilogue))) break;
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(d * p.bn);
       const int prow = kIsGrad ? grad_row(32 * q + lane) : 32 * q + lane;
       for (int c = 0; c * 32 < p.bn; ++c) {
+        const int lim = (int)min((int64_t)p.bn, e.M - m0) - c * 32;  // valid tokens from this chunk on
+        uint2 res[kMode == kLinear ? 8 : 1];
+        if (ahead) {  // on its way while the sums come out of tensor memory
+#pragma unroll
+          for (int s = 0; s < (kMode == kLinear ? 8 : 0); ++s)
+            if (t0 + s < lim) res[s] = residual4(e, m0 + c * 32 + t0 + s, n);
+        }
         uint32_t v[32];
         tmem_ld_32x32b_x32(acc + (uint32_t)(c * 32), v);
         tc_wait_ld();
@@ -578,42 +592,31 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 32; ++j) st[j * 128 + prow] = __uint_as_float(v[j]);
         bar_epilogue();
-        const int lim = (int)min((int64_t)p.bn, e.M - m0) - c * 32;  // valid tokens from this chunk on
         if (slot >= 0) {
           float *dst = p.part + ((int64_t)slot * p.bn + c * 32) * 128;
 #pragma unroll
           for (int s = 0; s < 8; ++s) {
-            const int t = s * 4 + (tid >> 5);
+            const int t = 8 * q + s;
             if (t < lim)
-              reinterpret_cast<float4 *>(dst + t * 128)[tid & 31] = reinterpret_cast<const float4 *>(st + t * 128)[tid & 31];
+              reinterpret_cast<float4 *>(dst + t * 128)[lane] = reinterpret_cast<const float4 *>(st + t * 128)[lane];
           }
-        } else if (kMode == kGated) {
-          if (n < e.N)
+        } else if (n < e.N) {
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              const int t = s * 16 + (tid >> 3);
-              if (t < lim) {
-                float x[8], g[8], u[8];
-                const float inv = sTok[c * 32 + t];
-                load8(st + t * 128 + 8 * (tid & 7), x);
-                scale8(x, c0, inv, g);
-                load8(st + t * 128 + 64 + 8 * (tid & 7), x);
-                scale8(x, c1, inv, u);
-                finish_gated(e, m0 + c * 32 + t, n, g, u);
+          for (int s = 0; s < kTok; ++s) {
+            const int t = t0 + s * kStep;
+            if (t < lim) {
+              const float inv = sTok[c * 32 + t];
+              float z[4];
+              c0.scale(*reinterpret_cast<const float4 *>(st + t * 128 + col), inv, z);
+              if constexpr (kMode == kGated) {
+                float u[4];
+                c1.scale(*reinterpret_cast<const float4 *>(st + t * 128 + 64 + col), inv, u);
+                finish_gated(e, m0 + c * 32 + t, n, z, u);
+              } else {
+                finish_linear(e, m0 + c * 32 + t, n, z, ahead, res[kMode == kLinear ? s : 0]);
               }
             }
-        } else {
-          if (n < e.N)
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-              const int t = s * 8 + (tid >> 4);
-              if (t < lim) {
-                float x[8], z[8];
-                load8(st + t * 128 + 8 * (tid & 15), x);
-                scale8(x, c0, sTok[c * 32 + t], z);
-                finish_linear(e, m0 + c * 32 + t, n, z);
-              }
-            }
+          }
         }
       }
       d ^= 1;
@@ -635,54 +638,51 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
 }
 
 // Sums the partial tiles of the tiles cut along the contraction, in order, and runs the
-// epilogue: one block per tile and 8 (gated: 16) tokens, 8 outputs per thread.
+// epilogue: one block per tile and 8 (gated: 16) tokens, 4 outputs per thread.
 template <int kMode>
-__global__ void __launch_bounds__(128) fused_finish(const FusedTcParams p) {
+__global__ void __launch_bounds__(256) fused_finish(const FusedTcParams p) {
   using namespace ftc;
   grid_dependency_wait();
-  constexpr int kTok = kMode == kGated ? 16 : 8, kPer = 128 / kTok;
+  constexpr int kTok = kMode == kGated ? 16 : 8, kPer = 256 / kTok;
   const FusedEpi &e = p.epi;
   const int t = blockIdx.x;  // among the cut tiles
   const int64_t total = (int64_t)(p.tiles - p.full) * p.units, u0 = (int64_t)t * p.units, u1 = u0 + p.units;
-  // the CTAs whose ranges [total c / C, total (c + 1) / C) meet [u0, u1)
-  auto begin = [&](int64_t c) { return total * c / p.tail_ctas; };
-  int64_t c0 = u0 * p.tail_ctas / total, c1 = c0;
+  // the CTAs whose ranges [total c / C, total (c + 1) / C) meet [u0, u1): a CTA's second
+  // piece is the start of a tile, its first one the rest of the tile before
+  auto begin = [&](int c) { return total * c / p.tail_ctas; };
+  int c0 = (int)(u0 * p.tail_ctas / total);
   while (begin(c0 + 1) <= u0) ++c0;
-  c1 = c0;
+  int c1 = c0;
   while (begin(c1 + 1) < u1) ++c1;
   if (c0 == c1) return;  // computed whole
+  const bool second = begin(c0) < u0;  // CTA c0 began in the tile before
   int row, tok;
   tile_at(p, p.full + t, row, tok);
-  const int tt = blockIdx.y * kTok + threadIdx.x / kPer, col = 8 * (threadIdx.x % kPer);
+  const int tt = blockIdx.y * kTok + threadIdx.x / kPer, col = 4 * (threadIdx.x % kPer);
   const int64_t m = (int64_t)tok * p.bn + tt;
   const int64_t n = kMode == kGated ? (int64_t)row * 64 + col : (int64_t)row * 128 + col;
   if (tt >= p.bn || m >= e.M || n >= e.N) return;
-  float v[8] = {}, w[8] = {};
-  for (int64_t c = c0; c <= c1; ++c) {
-    const int64_t slot = 2 * c + (begin(c) / p.units == t ? 0 : 1);
+  float4 v = make_float4(0, 0, 0, 0), w = v;
+  auto add = [](float4 &a, const float4 &x) { a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w; };
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const int64_t slot = 2 * c + (c == c0 && second ? 1 : 0);
     const float *src = p.part + (slot * p.bn + tt) * 128 + col;
-    float x[8];
-    load8(src, x);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += x[j];
-    if (kMode == kGated) {
-      load8(src + 64, x);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] += x[j];
-    }
+    add(v, *reinterpret_cast<const float4 *>(src));
+    if (kMode == kGated) add(w, *reinterpret_cast<const float4 *>(src + 64));
   }
   const float inv = e.tinv[m];
   ColK k;
-  float z[8];
+  float z[4];
   k.load(e, kMode == kGrad, n, n, e.N);
-  scale8(v, k, inv, z);
+  k.scale(v, inv, z);
   if (kMode == kGated) {
-    float u[8];
+    float u[4];
     k.load(e, false, e.N + n, n, e.N);
-    scale8(w, k, inv, u);
+    k.scale(w, inv, u);
     finish_gated(e, m, n, z, u);
   } else {
-    finish_linear(e, m, n, z);
+    finish_linear(e, m, n, z, false, make_uint2(0, 0));
   }
 }
 
@@ -697,7 +697,7 @@ cudaError_t launch_fused_tc_mode(const CUtensorMap &tmX, const CUtensorMap &tmP,
   e = launch_pdl(fused_tc_kernel<kMode>, dim3((unsigned)grid), dim3(ftc::kThreads), (size_t)smem, s, tmX, tmP, p);
   if (e != cudaSuccess || p.full == p.tiles) return e;
   const int tok = kMode == kGated ? 16 : 8;
-  return launch_pdl(fused_finish<kMode>, dim3((unsigned)(p.tiles - p.full), (unsigned)((p.bn + tok - 1) / tok)), dim3(128),
+  return launch_pdl(fused_finish<kMode>, dim3((unsigned)(p.tiles - p.full), (unsigned)((p.bn + tok - 1) / tok)), dim3(256),
                     (size_t)0, s, p);
 }
 

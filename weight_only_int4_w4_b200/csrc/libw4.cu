@@ -26,6 +26,7 @@
 #include "fused_stage.cu"
 #include "fused_tc.cu"
 #include "fused_gemv.cu"
+#include "fused_skinny.cu"
 #include "w4.h"
 
 namespace w4 {

@@ -376,7 +376,7 @@ def w4a16_gated_grad_workspace_size(M: int, F: int, K: int) -> int:
 
 _fused_ws: dict = {}
 _raw_stream = torch._C._cuda_getCurrentRawStream
-_DECODE_TOKENS = 16  # up to here, with groups of 128, a forward call needs no workspace
+_DECODE_TOKENS = 8  # up to here, with groups of 128, a forward call needs no workspace
 _X_DT = {torch.float16: W4_F16, torch.bfloat16: W4_BF16}
 
 
