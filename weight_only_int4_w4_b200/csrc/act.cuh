@@ -27,6 +27,30 @@ __device__ __forceinline__ float act_fwd(float x, int act) {
   }
 }
 
+// act of four values, one switch for all of them; GELU's erfc out of line, so that an epilogue
+// stays small: inlined for every value of an unrolled loop, the activations were most of
+// a kernel's instructions, and its epilogue waited for their way into the caches.
+__device__ __noinline__ float gelu_erf(float x) { return 0.5f * x * erfcf(-0.7071067811865476f * x); }
+__device__ __forceinline__ void act_fwd4(float (&z)[4], int act) {
+  if (act == kActNone) return;
+  if (act == kActRelu) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) z[j] = z[j] < 0.0f ? 0.0f : z[j];
+  } else if (act == kActGelu) {
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j) {
+      z[0] = gelu_erf(z[0]);  // one call in a loop that turns the four values round
+      const float t = z[0];
+      z[0] = z[1]; z[1] = z[2]; z[2] = z[3]; z[3] = t;
+    }
+  } else {
+    // x times the logistic function of x, or of 2 sqrt(2/pi) (x + 0.044715 x^3)
+    const float a = act == kActSilu ? 1.0f : 2.0f * kSqrt2OverPi, b = act == kActSilu ? 0.0f : kGeluCubic;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) z[j] *= logistic(a * fmaf(b * z[j], z[j] * z[j], z[j]));
+  }
+}
+
 // act(x) and act'(x)
 __device__ __forceinline__ void act_both(float x, int act, float &y, float &dy) {
   switch (act) {

@@ -34,7 +34,7 @@ size_t dtype_size(w4_dtype t) { return t == W4_F32 ? 4 : 2; }
 
 // Launch plan and workspace of a fused call.
 struct FusedPlan {
-  int bn = 16, mt = 1, rt = 1, units = 1, gt = 1, full = 0, tiles = 1, tail_ctas = 0, grid = 1;
+  int bn = 16, mt = 1, rt = 1, units = 1, gt = 1, full = 0, tiles = 1, tail_pairs = 0, pairs = 1;
   int64_t ld = 0;  // row stride of the staged operand
   size_t xp = 0, tinv = 0, rinv = 0, tab = 0, part = 0, dbias = 0, bytes = 0;
 };
@@ -45,29 +45,30 @@ constexpr int64_t kMinTailUnits = 4;
 // sizes whose tiles or blocks would not fit a grid are refused (false)
 bool fused_plan(int64_t M, int64_t N, int64_t K, bool gated, bool grad, int sm, FusedPlan &p) {
   const int64_t rows = grad ? K : gated ? N / 2 : N, depth = grad ? N : K;
-  const int64_t mt = cdiv(M, w4::ftc::kMaxBn), rt = cdiv(rows, gated && !grad ? 64 : 128), units = cdiv(depth, 128);
+  const int64_t mt = cdiv(M, w4::ftc::kMaxBn), rt = cdiv(rows, gated && !grad ? 128 : 256), units = cdiv(depth, 128);
+  const int pairs = sm / 2;
   if (M > (int64_t)1 << 30 || (double)rt * (double)mt > 1.0e9) return false;
   p.mt = (int)mt;
-  p.bn = (int)(cdiv(cdiv(M, mt), 16) * 16);
+  p.bn = (int)(cdiv(cdiv(M, mt), 32) * 32);
   p.rt = (int)rt;
   p.units = (int)units;
   p.gt = (int)std::min<int64_t>(mt, 8);
   p.tiles = (int)(rt * mt);
-  p.full = p.tiles / sm * sm;
+  p.full = p.tiles / pairs * pairs;
   const int64_t rest = p.tiles - p.full;
   if (rest > 0) {
-    const int64_t ctas = std::min<int64_t>(sm, rest * units / kMinTailUnits);
-    if (ctas > rest && rest * 10 < 9 * (int64_t)sm) p.tail_ctas = (int)ctas;
+    const int64_t share = std::min<int64_t>(pairs, rest * units / kMinTailUnits);
+    if (share > rest && rest * 10 < 9 * (int64_t)pairs) p.tail_pairs = (int)share;
     else p.full = p.tiles;
   }
-  p.grid = p.full > 0 ? std::min(sm, std::max(p.full, p.tail_ctas)) : p.tail_ctas;
+  p.pairs = p.full > 0 ? std::min(pairs, std::max(p.full, p.tail_pairs)) : p.tail_pairs;
   p.ld = grad ? cdiv(N, 8) * 8 : K;
   p.xp = kCounterBytes;
   p.tinv = p.xp + align256((size_t)M * p.ld * 2);
   p.rinv = p.tinv + align256((size_t)M * 4);
   p.tab = p.rinv + align256((size_t)N * 4);
   p.part = p.tab + align256((size_t)N * (K / 32) * 4);  // room for groups of 32
-  p.dbias = p.part + align256((size_t)2 * p.tail_ctas * p.bn * 128 * 4);
+  p.dbias = p.part + align256((size_t)4 * p.tail_pairs * p.bn * 128 * 4);
   const size_t db = !grad ? 0 : (size_t)w4::fused_dbias_parts(M, N, gated, sm) * N * 4;
   p.bytes = p.dbias + align256(db);
   return true;
@@ -228,7 +229,7 @@ w4_status fused_run_tc(const FusedCall &c, const FusedPlan &plan, int sm, cudaSt
   const int64_t kg = c.K / c.group, depth = c.grad ? plan.ld : c.K;
   CUtensorMap tmX, tmP;
   CUresult r = encode_2d(enc, &tmX, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, xp, (uint64_t)depth, (uint64_t)c.M,
-                         (uint64_t)plan.ld * 2, 64u, (uint32_t)plan.bn, CU_TENSOR_MAP_SWIZZLE_128B,
+                         (uint64_t)plan.ld * 2, 64u, (uint32_t)plan.bn / 2, CU_TENSOR_MAP_SWIZZLE_128B,
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
   if (r != CUDA_SUCCESS) return fail(W4_ERR_CUDA, "tensor map for staged operands failed (CUresult %d)", (int)r);
   r = encode_2d(enc, &tmP, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.packed, (uint64_t)(c.K / 2), (uint64_t)c.N,
@@ -259,9 +260,9 @@ w4_status fused_run_tc(const FusedCall &c, const FusedPlan &plan, int sm, cudaSt
   p.rows = c.N; p.kg = kg;
   p.gshift = c.group == 128 ? 7 : c.group == 64 ? 6 : 5;
   p.bn = plan.bn; p.mt = plan.mt; p.rt = plan.rt; p.units = plan.units; p.gt = plan.gt;
-  p.full = plan.full; p.tiles = plan.tiles; p.tail_ctas = plan.tail_ctas;
+  p.full = plan.full; p.tiles = plan.tiles; p.tail_pairs = plan.tail_pairs;
   p.part = reinterpret_cast<float *>(ws + plan.part);
-  e = w4::launch_fused_tc(c.grad ? w4::kGrad : c.gated ? w4::kGated : w4::kLinear, tmX, tmP, p, plan.grid, s);
+  e = w4::launch_fused_tc(c.grad ? w4::kGrad : c.gated ? w4::kGated : w4::kLinear, tmX, tmP, p, plan.pairs, s);
   if (e != cudaSuccess) return cuda_fail(e, "fused product launch");
   if (c.dbias) {
     e = w4::launch_fused_dbias_sum(c.M, c.N, c.gated, reinterpret_cast<const float *>(ws + plan.dbias), c.dbias, sm, s);

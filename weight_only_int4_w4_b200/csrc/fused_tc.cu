@@ -53,22 +53,22 @@ struct FusedTcParams {
   int64_t rows;             // packed rows
   int64_t kg;               // groups per packed row
   int gshift;               // log2(group)
-  int bn, mt, rt, units;    // token tile, token tiles, row tiles, 128-deep units per tile
+  int bn, mt, rt, units;    // token tile, token tiles, pairs of row tiles, 128-deep units per tile
   int gt;                   // token tiles per raster block
   int full;                 // tiles computed whole
-  int tiles, tail_ctas;     // all tiles; CTAs that share the rest
-  float *part;              // [2 * tail_ctas][bn][128] partial tiles
+  int tiles, tail_pairs;    // all tiles (of 256 rows); CTA pairs that share the rest
+  float *part;              // [2 * tail_pairs][2 CTAs][bn][128] partial tiles
 };
 
 namespace ftc {
 
-constexpr int kSets = 3;                 // dequantizing sets of four warps, one A buffer each
+constexpr int kSets = 4;                 // dequantizing sets of four warps, one A buffer each
 constexpr int kThreads = 256 + kSets * 128;
 constexpr int kCodeStages = 4, kCodeStage = 128 * 64;
-constexpr int kAct = 64 * 2;             // bytes of a token's 64 channels in a stage
+constexpr int kAct = 64 * 2 / 2;         // bytes of a token's 64 channels in a stage, half of the tokens to a CTA
 constexpr int kStageOut = 32 * 128 * 4;  // 32 tokens of a tile in fp32
 constexpr int kGradAStage = 64 * 128 * 2;
-constexpr int kMaxBn = 208;
+constexpr int kMaxBn = 192;              // a multiple of 32
 constexpr int kMaxActStages = 8;
 
 __host__ __device__ constexpr int fixed_bytes(bool grad) {
@@ -85,16 +85,63 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T
-__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
+// Products of a CTA pair (M = 256: 128 rows in each CTA's tensor memory), issued by one
+// thread of the pair's first CTA: D (+)= A B^T with A in tensor or shared memory.
+__device__ __forceinline__ void pair_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void pair_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
+// Arrives at the barrier of the same place in both CTAs once the products issued so far are done.
+__device__ __forceinline__ void pair_commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                   smem_u32(bar)),
+               "h"((uint16_t)3)
+               : "memory");
+}
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t *dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The shared::cluster address of the first CTA's barrier of the same place.
+__device__ __forceinline__ uint32_t first_cta(const uint64_t *bar) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(bar)));
+  return a;
+}
+// (Release at the scope of the CTA: what the pair shares is tensor memory and operands read by
+// the async proxy, which the fences in front order.  At cluster scope each arrive waited
+// some 1,700 cycles for its warp's loads in flight.)
+__device__ __forceinline__ void arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// A TMA load into this CTA's memory (no multicast) that completes at a barrier of either CTA.
+__device__ __forceinline__ void pair_tma_load(void *dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
 // Whether the phase is complete, without waiting (try_wait may suspend the thread for
 // microseconds).
 __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
@@ -170,18 +217,20 @@ __device__ __forceinline__ void dequant8(uint32_t w, const GroupK &g, uint32_t (
   o[3] = hmul2(hfma2(d, k16th, g.zhi), g.s);
 }
 
-// One CTA's share of the work: tiles blockIdx, blockIdx + grid, ... below `full`, then its
+// A CTA pair's share of the work: tiles pair, pair + pairs, ... below `full`, then its
 // range of the remaining tiles' units.  slot < 0: a whole tile.
 struct Work {
   const FusedTcParams &p;
   int t;
   int64_t u, u1, base;
   int nth;
-  __device__ __forceinline__ explicit Work(const FusedTcParams &q) : p(q), t(blockIdx.x), u(0), u1(0), nth(0) {
-    if ((int)blockIdx.x < p.tail_ctas) {
+  int pair, pairs;
+  __device__ __forceinline__ explicit Work(const FusedTcParams &q)
+      : p(q), t(blockIdx.x >> 1), u(0), u1(0), nth(0), pair(blockIdx.x >> 1), pairs(gridDim.x >> 1) {
+    if (pair < p.tail_pairs) {
       const int64_t total = (int64_t)(p.tiles - p.full) * p.units;
-      u = total * blockIdx.x / p.tail_ctas;
-      u1 = total * (blockIdx.x + 1) / p.tail_ctas;
+      u = total * pair / p.tail_pairs;
+      u1 = total * (pair + 1) / p.tail_pairs;
     }
   }
   __device__ __forceinline__ bool next(int &tile, int &k0, int &k1, int &slot) {
@@ -190,7 +239,7 @@ struct Work {
       k0 = 0;
       k1 = p.units;
       slot = -1;
-      t += gridDim.x;
+      t += pairs;
       return true;
     }
     if (u >= u1) return false;
@@ -199,7 +248,7 @@ struct Work {
     k0 = (int)(u - (int64_t)i * p.units);
     k1 = (int)min((int64_t)p.units, k0 + (u1 - u));
     u += k1 - k0;
-    slot = k1 - k0 == p.units ? -1 : 2 * (int)blockIdx.x + nth;
+    slot = k1 - k0 == p.units ? -1 : 2 * pair + nth;
     ++nth;
     return true;
   }
@@ -207,46 +256,49 @@ struct Work {
 
 // Raster: blocks of gt token tiles, inside a block the token tiles of one row tile side
 // by side, so that the CTAs at work at one time share activations and weights in L2.
-__device__ __forceinline__ void tile_at(const FusedTcParams &p, int t, int &row, int &tok) {
+__device__ __forceinline__ void tile_at(const FusedTcParams &p, int t, int rank, int &row, int &tok) {
   const int per = p.gt * p.rt, g = t / per, r = t - g * per;
   const int w = min(p.gt, p.mt - g * p.gt);
-  row = r / w;
-  tok = g * p.gt + r - row * w;
+  const int pr = r / w;
+  tok = g * p.gt + r - pr * w;
+  row = 2 * pr + rank;
 }
 
 // The k that tile row r of a gradient tile holds: the dequantization's pairs put code
 // {0,4,1,5,2,6,3,7}[j] of a word at place j.
 __device__ __forceinline__ int grad_row(int r) { return (r & ~7) | ((r & 1) << 2) | ((r >> 1) & 3); }
 
+// 16-bit types both ways without a branch: both conversions, and the one that counts.
 __device__ __forceinline__ void widen4(const uint2 &w, int dtype, float (&v)[4]) {
-  if (dtype == 2) {
-    v[0] = __uint_as_float(w.x << 16);
-    v[1] = __uint_as_float(w.x & 0xFFFF0000u);
-    v[2] = __uint_as_float(w.y << 16);
-    v[3] = __uint_as_float(w.y & 0xFFFF0000u);
-  } else {
-    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&w.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
-    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
-  }
+  const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&w.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
+  const bool bf16 = dtype == 2;
+  v[0] = bf16 ? __uint_as_float(w.x << 16) : a.x;
+  v[1] = bf16 ? __uint_as_float(w.x & 0xFFFF0000u) : a.y;
+  v[2] = bf16 ? __uint_as_float(w.y << 16) : b.x;
+  v[3] = bf16 ? __uint_as_float(w.y & 0xFFFF0000u) : b.y;
+}
+__device__ __forceinline__ uint32_t narrow2(float a, float b, int dtype) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+  return dtype == 2 ? *reinterpret_cast<const uint32_t *>(&x) : half2_bits(a, b);
+}
+
+// One value at a time: rows that do not start on a vector.
+__device__ __noinline__ void put4_slow(void *p, int dtype, int64_t at, int count, float a, float b, float c, float d) {
+  const float v[4] = {a, b, c, d};
+#pragma unroll 1
+  for (int j = 0; j < count; ++j) store_from_float(p, dtype, at + j, j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[2] : v[3]);
 }
 
 // Stores v at columns n.. of a row that starts at element `row`; n + j < lim.
 __device__ __forceinline__ void put4(void *p, int dtype, int64_t row, int64_t n, int64_t lim, bool vec, const float (&v)[4]) {
-  if (vec) {  // lim is a multiple of 4
-    if (dtype == 0) {
-      *reinterpret_cast<float4 *>(static_cast<float *>(p) + row + n) = make_float4(v[0], v[1], v[2], v[3]);
-    } else if (dtype == 1) {
-      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + row + n) = make_uint2(half2_bits(v[0], v[1]), half2_bits(v[2], v[3]));
-    } else {
-      const __nv_bfloat162 x = __floats2bfloat162_rn(v[0], v[1]), y = __floats2bfloat162_rn(v[2], v[3]);
-      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + row + n) =
-          make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
-    }
+  if (!vec) {  // else lim is a multiple of 4
+    put4_slow(p, dtype, row + n, (int)min((int64_t)4, lim - n), v[0], v[1], v[2], v[3]);
+  } else if (dtype != 0) {
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + row + n) =
+        make_uint2(narrow2(v[0], v[1], dtype), narrow2(v[2], v[3], dtype));
   } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (n + j < lim) store_from_float(p, dtype, row + n + j, v[j]);
+    *reinterpret_cast<float4 *>(static_cast<float *>(p) + row + n) = make_float4(v[0], v[1], v[2], v[3]);
   }
 }
 
@@ -280,19 +332,19 @@ __device__ __forceinline__ uint2 residual4(const FusedEpi &e, int64_t m, int64_t
 __device__ __forceinline__ void finish_linear(const FusedEpi &e, int64_t m, int64_t n, float (&z)[4], bool have, const uint2 &res) {
   const int64_t row = m * e.N;
   if (e.Z) put4(e.Z, e.z_dtype, row, n, e.N, e.vec, z);
-  if (e.act != kActNone) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) z[j] = act_fwd(z[j], e.act);
-  }
+  act_fwd4(z, e.act);
   if (have) {
     float a[4];
     widen4(res, e.y_dtype, a);
 #pragma unroll
     for (int j = 0; j < 4; ++j) z[j] += a[j];
-  } else if (e.residual) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (n + j < e.N) z[j] += load_as_float(e.residual, e.y_dtype, row + n + j);
+  } else if (e.residual) {  // fp32, or rows that do not start on a vector
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j) {
+      z[0] += n + j < e.N ? load_as_float(e.residual, e.y_dtype, row + n + j) : 0.0f;
+      const float t = z[0];  // the four values turn round
+      z[0] = z[1]; z[1] = z[2]; z[2] = z[3]; z[3] = t;
+    }
   }
   put4(e.Y, e.y_dtype, row, n, e.N, e.vec, z);
 }
@@ -302,8 +354,9 @@ __device__ __forceinline__ void finish_gated(const FusedEpi &e, int64_t m, int64
     put4(e.Z, e.z_dtype, m * 2 * e.N, f, e.N, e.vec, g);
     put4(e.Z, e.z_dtype, m * 2 * e.N + e.N, f, e.N, e.vec, u);
   }
+  act_fwd4(g, e.act);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) g[j] = act_fwd(g[j], e.act) * u[j];
+  for (int j = 0; j < 4; ++j) g[j] *= u[j];
   put4(e.Y, e.y_dtype, m * e.N, f, e.N, e.vec, g);
 }
 
@@ -333,9 +386,10 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
 
+  const int rank = (int)(blockIdx.x & 1);
   if (threadIdx.x == 0) {
     for (int i = 0; i < ns; ++i) {
-      mbar_init(&full[i], 1 + 128);  // the activations' box, and the set that converts the block
+      mbar_init(&full[i], 1 + 8);  // the first CTA's: both boxes of activations, and a set's 4 warps in each CTA
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < kCodeStages; ++i) {
@@ -344,18 +398,16 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&dfull[i], 1);
-      mbar_init(&dempty[i], 128);
+      mbar_init(&dempty[i], 8);  // the first CTA's: the epilogue's warps of both
     }
     fence_barrier_init();
     prefetch_tensormap(&tmX);
     prefetch_tensormap(&tmP);
   }
-  if (warp == 3) {
-    tmem_alloc(holder, 512);
-    tmem_relinquish();
-  }
+  if (warp == 3) pair_tmem_alloc(holder, 512);
   tc_fence_before();
   __syncthreads();
+  pair_sync();  // the other CTA's barriers are there before anything arrives at them
   tc_fence_after();
   const uint32_t tmem = *holder;
   bool ok = true;
@@ -363,18 +415,18 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
   Work work(p);
   int tile, k0, k1, slot;
   if (warp == 0) {
-    // ---- activations: one box of BN tokens x 64 per stage
+    // ---- activations: a box of half the tile's tokens x 64 per stage and CTA
     grid_dependency_wait();
     int s = 0;
     uint32_t ph = 0;
     while (ok && work.next(tile, k0, k1, slot)) {
       int row, tok;
-      tile_at(p, tile, row, tok);
+      tile_at(p, tile, rank, row, tok);
       for (int b = 2 * k0; b < 2 * k1; ++b) {
         if (!wait_all(&empty[s], ph ^ 1u, kErrTimeoutTma)) { ok = false; break; }
         if (elect_one()) {
-          mbar_arrive_expect_tx(&full[s], (uint32_t)act_stage);
-          tma_load_2d(sX + s * act_stage, &tmX, &full[s], b * 64, tok * p.bn);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(2 * act_stage));
+          pair_tma_load(sX + s * act_stage, &tmX, first_cta(&full[s]), b * 64, tok * p.bn + rank * (p.bn / 2));
         }
         __syncwarp();
         if (++s == ns) s = 0, ph ^= 1u;
@@ -386,7 +438,7 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
     uint32_t ph = 0;
     while (ok && work.next(tile, k0, k1, slot)) {
       int row, tok;
-      tile_at(p, tile, row, tok);
+      tile_at(p, tile, rank, row, tok);
       for (int u = k0; u < k1; ++u) {
         if (!wait_all(&cempty[s], ph ^ 1u, kErrTimeoutTma)) { ok = false; break; }
         if (elect_one()) {
@@ -405,9 +457,9 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
         if (++s == kCodeStages) s = 0, ph ^= 1u;
       }
     }
-  } else if (warp == 2) {
-    // ---- products
-    const uint32_t idesc = idesc_f16(false, p.bn) | (kIsGrad ? 1u << 15 : 0u);  // bit 15: A is MN-major
+  } else if (warp == 2 && rank == 0) {
+    // ---- products of both CTAs: M = 256; bit 15: A is MN-major
+    const uint32_t idesc = (idesc_f16(false, p.bn) + ((uint32_t)(128 >> 4) << 24)) | (kIsGrad ? 1u << 15 : 0u);
     int s = 0, a = 0, d = 0;
     uint32_t ph = 0, dph = 0;
     bool ready = false;  // the barrier of the block at hand was seen complete while the last one was issued
@@ -430,15 +482,15 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
                                 ((uint64_t)(8192 >> 4) << 16);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              tc_mma_ss(acc, ad + (uint64_t)(128 * j), bd + (uint64_t)(2 * j), idesc, b == 2 * k0 && j == 0 ? 0u : 1u);
+              pair_mma_ss(acc, ad + (uint64_t)(128 * j), bd + (uint64_t)(2 * j), idesc, b == 2 * k0 && j == 0 ? 0u : 1u);
           } else {
             const uint32_t at = tmem + (uint32_t)(2 * p.bn + 32 * a);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              tc_mma_ts(acc, at + 8 * j, bd + (uint64_t)(2 * j), idesc, b == 2 * k0 && j == 0 ? 0u : 1u);
+              pair_mma_ts(acc, at + 8 * j, bd + (uint64_t)(2 * j), idesc, b == 2 * k0 && j == 0 ? 0u : 1u);
           }
-          tc_commit(done);
-          if (b == 2 * k1 - 1) tc_commit(&dfull[d]);
+          pair_commit(done);
+          if (b == 2 * k1 - 1) pair_commit(&dfull[d]);
         }
         __syncwarp();
         if (++a == kSets) a = 0;
@@ -466,7 +518,7 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
         b -= b1;
         if (!work.next(tile, k0, k1, slot)) return false;
         int tok;
-        tile_at(p, tile, row, tok);
+        tile_at(p, tile, rank, row, tok);
         b += 2 * k0;
         b1 = 2 * k1;
         if constexpr (kMode == kLinear) {
@@ -536,7 +588,8 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
         tc_wait_st();
         tc_fence_before();
       }
-      mbar_arrive(&full[s]);
+      __syncwarp();
+      if (elect_one()) arrive_cluster(first_cta(&full[s]));
       // The codes are given back only here, behind the stores that needed them: an arrive
       // right behind the loads let the loads sink below it, and now and then read the
       // stage's next contents.
@@ -555,12 +608,13 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
     uint32_t dph = 0;
     while (work.next(tile, k0, k1, slot)) {
       int row, tok;
-      tile_at(p, tile, row, tok);
+      tile_at(p, tile, rank, row, tok);
       const int64_t m0 = (int64_t)tok * p.bn;
       for (int t = tid; t < p.bn; t += 128) sTok[t] = m0 + t < e.M ? e.tinv[m0 + t] : 0.0f;
       // four columns of the tile (gated: and the same of the up half), and with 32 (16)
       // lanes to a token, a warp's 8 tokens of a chunk of 32
       constexpr int kLanes = kMode == kGated ? 16 : 32, kTok = 8 * kLanes / 32, kStep = 32 / kLanes;
+      constexpr int kGroup4 = kMode == kLinear ? 4 : 2;
       const int col = 4 * (lane & (kLanes - 1)), t0 = 8 * q + lane / kLanes;
       const int64_t n = (int64_t)row * (kMode == kGated ? 64 : 128) + col;
       ColK c0, c1;
@@ -575,25 +629,28 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
       const int prow = kIsGrad ? grad_row(32 * q + lane) : 32 * q + lane;
       for (int c = 0; c * 32 < p.bn; ++c) {
         const int lim = (int)min((int64_t)p.bn, e.M - m0) - c * 32;  // valid tokens from this chunk on
-        uint2 res[kMode == kLinear ? 8 : 1];
-        if (ahead) {  // on its way while the sums come out of tensor memory
+        uint2 res[4];
+        auto read_ahead = [&](int s0) {  // the residuals of four of this thread's tokens
+          if (ahead)
 #pragma unroll
-          for (int s = 0; s < (kMode == kLinear ? 8 : 0); ++s)
-            if (t0 + s < lim) res[s] = residual4(e, m0 + c * 32 + t0 + s, n);
-        }
+            for (int s = 0; s < 4; ++s)
+              if (t0 + s0 + s < lim) res[s] = residual4(e, m0 + c * 32 + t0 + s0 + s, n);
+        };
+        if constexpr (kMode == kLinear) read_ahead(0);  // on their way while the sums come out of tensor memory
         uint32_t v[32];
         tmem_ld_32x32b_x32(acc + (uint32_t)(c * 32), v);
         tc_wait_ld();
         if ((c + 1) * 32 >= p.bn) {
           tc_fence_before();
-          mbar_arrive(&dempty[d]);
+          __syncwarp();
+          if (elect_one()) arrive_cluster(first_cta(&dempty[d]));
         }
         float *st = sOut + (c & 1) * (kStageOut / 4);
 #pragma unroll
         for (int j = 0; j < 32; ++j) st[j * 128 + prow] = __uint_as_float(v[j]);
         bar_epilogue();
         if (slot >= 0) {
-          float *dst = p.part + ((int64_t)slot * p.bn + c * 32) * 128;
+          float *dst = p.part + (((int64_t)slot * 2 + rank) * p.bn + c * 32) * 128;
 #pragma unroll
           for (int s = 0; s < 8; ++s) {
             const int t = 8 * q + s;
@@ -601,19 +658,27 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
               reinterpret_cast<float4 *>(dst + t * 128)[lane] = reinterpret_cast<const float4 *>(st + t * 128)[lane];
           }
         } else if (n < e.N) {
+          // (loops of few tokens: a long epilogue waits for its instructions, see act_fwd4)
+#pragma unroll 1
+          for (int s0 = 0; s0 < kTok; s0 += kGroup4) {
+            uint2 now[kGroup4];
 #pragma unroll
-          for (int s = 0; s < kTok; ++s) {
-            const int t = t0 + s * kStep;
-            if (t < lim) {
-              const float inv = sTok[c * 32 + t];
-              float z[4];
-              c0.scale(*reinterpret_cast<const float4 *>(st + t * 128 + col), inv, z);
-              if constexpr (kMode == kGated) {
-                float u[4];
-                c1.scale(*reinterpret_cast<const float4 *>(st + t * 128 + 64 + col), inv, u);
-                finish_gated(e, m0 + c * 32 + t, n, z, u);
-              } else {
-                finish_linear(e, m0 + c * 32 + t, n, z, ahead, res[kMode == kLinear ? s : 0]);
+            for (int s = 0; s < kGroup4; ++s) now[s] = res[s];
+            if (kMode == kLinear && s0 + kGroup4 < kTok) read_ahead(s0 + kGroup4);
+#pragma unroll
+            for (int s = 0; s < kGroup4; ++s) {
+              const int t = t0 + (s0 + s) * kStep;
+              if (t < lim) {
+                const float inv = sTok[c * 32 + t];
+                float z[4];
+                c0.scale(*reinterpret_cast<const float4 *>(st + t * 128 + col), inv, z);
+                if constexpr (kMode == kGated) {
+                  float u[4];
+                  c1.scale(*reinterpret_cast<const float4 *>(st + t * 128 + 64 + col), inv, u);
+                  finish_gated(e, m0 + c * 32 + t, n, z, u);
+                } else {
+                  finish_linear(e, m0 + c * 32 + t, n, z, ahead, now[s]);
+                }
               }
             }
           }
@@ -631,9 +696,10 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  pair_sync();  // neither CTA leaves while the other's products read or arrive here
   if (warp == 3) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    pair_tmem_dealloc(tmem, 512);
   }
 }
 
@@ -645,19 +711,19 @@ __global__ void __launch_bounds__(256) fused_finish(const FusedTcParams p) {
   grid_dependency_wait();
   constexpr int kTok = kMode == kGated ? 16 : 8, kPer = 256 / kTok;
   const FusedEpi &e = p.epi;
-  const int t = blockIdx.x;  // among the cut tiles
+  const int t = blockIdx.x >> 1, rank = blockIdx.x & 1;  // among the cut tiles; the pair's CTA
   const int64_t total = (int64_t)(p.tiles - p.full) * p.units, u0 = (int64_t)t * p.units, u1 = u0 + p.units;
-  // the CTAs whose ranges [total c / C, total (c + 1) / C) meet [u0, u1): a CTA's second
+  // the pairs whose ranges [total c / C, total (c + 1) / C) meet [u0, u1): a pair's second
   // piece is the start of a tile, its first one the rest of the tile before
-  auto begin = [&](int c) { return total * c / p.tail_ctas; };
-  int c0 = (int)(u0 * p.tail_ctas / total);
+  auto begin = [&](int c) { return total * c / p.tail_pairs; };
+  int c0 = (int)(u0 * p.tail_pairs / total);
   while (begin(c0 + 1) <= u0) ++c0;
   int c1 = c0;
   while (begin(c1 + 1) < u1) ++c1;
   if (c0 == c1) return;  // computed whole
-  const bool second = begin(c0) < u0;  // CTA c0 began in the tile before
+  const bool second = begin(c0) < u0;  // pair c0 began in the tile before
   int row, tok;
-  tile_at(p, p.full + t, row, tok);
+  tile_at(p, p.full + t, rank, row, tok);
   const int tt = blockIdx.y * kTok + threadIdx.x / kPer, col = 4 * (threadIdx.x % kPer);
   const int64_t m = (int64_t)tok * p.bn + tt;
   const int64_t n = kMode == kGated ? (int64_t)row * 64 + col : (int64_t)row * 128 + col;
@@ -667,7 +733,7 @@ __global__ void __launch_bounds__(256) fused_finish(const FusedTcParams p) {
 #pragma unroll 4
   for (int c = c0; c <= c1; ++c) {
     const int64_t slot = 2 * c + (c == c0 && second ? 1 : 0);
-    const float *src = p.part + (slot * p.bn + tt) * 128 + col;
+    const float *src = p.part + ((slot * 2 + rank) * p.bn + tt) * 128 + col;
     add(v, *reinterpret_cast<const float4 *>(src));
     if (kMode == kGated) add(w, *reinterpret_cast<const float4 *>(src + 64));
   }
@@ -687,25 +753,38 @@ __global__ void __launch_bounds__(256) fused_finish(const FusedTcParams p) {
 }
 
 template <int kMode>
-cudaError_t launch_fused_tc_mode(const CUtensorMap &tmX, const CUtensorMap &tmP, const FusedTcParams &p, int grid,
+cudaError_t launch_fused_tc_mode(const CUtensorMap &tmX, const CUtensorMap &tmP, const FusedTcParams &p, int pairs,
                                  cudaStream_t s) {
   static std::atomic<int> attr[kAttrDevices];
   constexpr bool grad = kMode == kGrad;
   const int smem = ftc::fixed_bytes(grad) + ftc::act_stages(p.bn, grad) * p.bn * ftc::kAct;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(fused_tc_kernel<kMode>), smem, attr);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(fused_tc_kernel<kMode>, dim3((unsigned)grid), dim3(ftc::kThreads), (size_t)smem, s, tmX, tmP, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
+  cfg.blockDim = dim3(ftc::kThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = 2;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, fused_tc_kernel<kMode>, tmX, tmP, p);
   if (e != cudaSuccess || p.full == p.tiles) return e;
   const int tok = kMode == kGated ? 16 : 8;
-  return launch_pdl(fused_finish<kMode>, dim3((unsigned)(p.tiles - p.full), (unsigned)((p.bn + tok - 1) / tok)), dim3(256),
+  return launch_pdl(fused_finish<kMode>, dim3((unsigned)(2 * (p.tiles - p.full)), (unsigned)((p.bn + tok - 1) / tok)), dim3(256),
                     (size_t)0, s, p);
 }
 
-cudaError_t launch_fused_tc(int mode, const CUtensorMap &tmX, const CUtensorMap &tmP, const FusedTcParams &p, int grid,
+cudaError_t launch_fused_tc(int mode, const CUtensorMap &tmX, const CUtensorMap &tmP, const FusedTcParams &p, int pairs,
                             cudaStream_t s) {
-  return mode == kLinear  ? launch_fused_tc_mode<kLinear>(tmX, tmP, p, grid, s)
-         : mode == kGated ? launch_fused_tc_mode<kGated>(tmX, tmP, p, grid, s)
-                          : launch_fused_tc_mode<kGrad>(tmX, tmP, p, grid, s);
+  return mode == kLinear  ? launch_fused_tc_mode<kLinear>(tmX, tmP, p, pairs, s)
+         : mode == kGated ? launch_fused_tc_mode<kGated>(tmX, tmP, p, pairs, s)
+                          : launch_fused_tc_mode<kGrad>(tmX, tmP, p, pairs, s);
 }
 
 }  // namespace w4
