@@ -40,7 +40,7 @@ struct FusedPlan {
 };
 
 // Fragments of a cut tile hold at least this many 128-deep units.
-constexpr int64_t kMinTailUnits = 4;
+constexpr int64_t kMinTailUnits = 2;
 
 // sizes whose tiles or blocks would not fit a grid are refused (false)
 bool fused_plan(int64_t M, int64_t N, int64_t K, bool gated, bool grad, int sm, FusedPlan &p) {
@@ -237,10 +237,11 @@ w4_status fused_run_tc(const FusedCall &c, const FusedPlan &plan, int sm, cudaSt
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
   if (r != CUDA_SUCCESS) return fail(W4_ERR_CUDA, "tensor map for packed weights failed (CUresult %d)", (int)r);
   cudaError_t e;
+  int64_t sums = 0;  // rows of dbias's partial sums that are still to be added
   if (c.grad) {
     e = w4::launch_fused_stage_dz(c.X, c.act == W4_ACT_NONE && !c.gated ? nullptr : c.Z, (int)c.x_dtype, (int)c.act,
                                   c.gated, c.M, c.N, plan.ld, c.scales, c.zeros, kg, xp, tinv, rinv, tab,
-                                  reinterpret_cast<float *>(ws + plan.dbias), c.dbias, sm, s);
+                                  reinterpret_cast<float *>(ws + plan.dbias), c.dbias, sm, &sums, s);
   } else {
     e = w4::launch_fused_stage_x(c.X, c.x_dtype == W4_BF16, c.awq_s, c.M, c.K, c.scales, c.zeros, kg, c.N, xp, tinv, rinv,
                                  tab, s);
@@ -265,7 +266,7 @@ w4_status fused_run_tc(const FusedCall &c, const FusedPlan &plan, int sm, cudaSt
   e = w4::launch_fused_tc(c.grad ? w4::kGrad : c.gated ? w4::kGated : w4::kLinear, tmX, tmP, p, plan.pairs, s);
   if (e != cudaSuccess) return cuda_fail(e, "fused product launch");
   if (c.dbias) {
-    e = w4::launch_fused_dbias_sum(c.M, c.N, c.gated, reinterpret_cast<const float *>(ws + plan.dbias), c.dbias, sm, s);
+    e = w4::launch_fused_dbias_sum(c.N, sums, reinterpret_cast<const float *>(ws + plan.dbias), c.dbias, s);
     if (e != cudaSuccess) return cuda_fail(e, "bias gradient launch");
   }
   return W4_OK;

@@ -69,10 +69,10 @@ __device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n) {
 // Blocks 0..bn-1: one token each (zeros behind the last).  x' as in fused_stage_x, as
 // [K / 64][bn][64] fp16; 1 / 2^b.
 template <bool kBf16>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
     fused_stage_small(const uint16_t *X, const float *awq_s, int64_t M, int64_t K, int bn, uint16_t *xp, float *tinv) {
   grid_launch_dependents();
-  __shared__ float red[8];
+  __shared__ float red[32];
   const int64_t m = blockIdx.x, nv = K / 8;
   const bool real = m < M;
   const uint4 *row = reinterpret_cast<const uint4 *>(X + m * K);
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(256)
   float mx = 0.0f;
   if (real)
 #pragma unroll 4
-    for (int64_t v = threadIdx.x; v < nv; v += 256) {
+    for (int64_t v = threadIdx.x; v < nv; v += blockDim.x) {
       float f[8];
       scaled(v, f);
 #pragma unroll
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(256)
   const float2 e = pow2_to(block_max(mx, red), 13);
   if (threadIdx.x == 0) tinv[m] = e.y;
 #pragma unroll 4
-  for (int64_t v = threadIdx.x; v < nv; v += 256) {
+  for (int64_t v = threadIdx.x; v < nv; v += blockDim.x) {
     float f[8];
     scaled(v, f);
     *reinterpret_cast<uint4 *>(xp + ((v >> 3) * bn + m) * 64 + (v & 7) * 8) =
@@ -437,8 +437,9 @@ __global__ void __launch_bounds__(fsk::kThreads, 1)
 cudaError_t launch_fused_stage_small(const void *X, bool bf16, const float *awq_s, int64_t M, int64_t K, int bn, uint16_t *xp,
                                      float *tinv, cudaStream_t s) {
   const uint16_t *x = static_cast<const uint16_t *>(X);
-  if (bf16) fused_stage_small<true><<<bn, 256, 0, s>>>(x, awq_s, M, K, bn, xp, tinv);
-  else fused_stage_small<false><<<bn, 256, 0, s>>>(x, awq_s, M, K, bn, xp, tinv);
+  const int threads = K >= 8192 ? 1024 : K >= 4096 ? 512 : 256;  // two vectors or so to a thread
+  if (bf16) fused_stage_small<true><<<bn, threads, 0, s>>>(x, awq_s, M, K, bn, xp, tinv);
+  else fused_stage_small<false><<<bn, threads, 0, s>>>(x, awq_s, M, K, bn, xp, tinv);
   return cudaGetLastError();
 }
 

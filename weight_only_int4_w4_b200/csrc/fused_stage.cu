@@ -200,71 +200,88 @@ __device__ __forceinline__ void dz_at(const void *dY, const void *Z, int dtype, 
 }
 
 // dz' = fp16(dZ / r[n] * e), natural order, and 1 / e.  A cluster of CTAs takes tokens in turn,
-// each CTA the same 512 kDzVecs outputs f (of a gated call: rows f and F + f, which share
-// their inputs) of every token: dZ stays in registers while the CTAs exchange the token's
-// largest value, the next token's inputs are on their way meanwhile, and dbias's sums
-// over the cluster's tokens, to part [cluster][N], cost nothing but additions.
-constexpr int kDzThreads = 256, kDzVecs = 2, kDzSlice = kDzThreads * kDzVecs * 8;
+// each CTA the same 256 V vectors of 8 outputs f (of a gated call: rows f and F + f, which
+// share their inputs) of every token: dZ stays in registers while the CTAs exchange the
+// token's largest value, the next token's inputs are on their way meanwhile, and dbias's
+// sums over the cluster's tokens, to part [cluster][N], cost nothing but additions.
+// V = 1 where a cluster of 8 reaches over F with it (more CTAs then hide each other's
+// exchanges), else 2.  kVec: rows start on 16 bytes; else elements one at a time.
+constexpr int kDzThreads = 256;
 
-template <bool kGated, bool kBias>
-__global__ void __launch_bounds__(kDzThreads, 2)
-    fused_stage_dz(const uint16_t *dY, const uint16_t *Z, int bf16, int act, int64_t M, int64_t N, const float *rinv,
-                   uint16_t *dzp, float *tinv, float *part) {
-  constexpr int R = kGated ? 2 : 1;
-  __shared__ __align__(16) float srinv[R][kDzSlice];
+template <bool kGated, bool kBias, bool kVec, int V>
+__global__ void __launch_bounds__(kDzThreads, V == 1 ? 3 : 2)
+    fused_stage_dz(const uint16_t *dY, const uint16_t *Z, int bf16, int act, int64_t M, int64_t N, int64_t ld,
+                   const float *rinv, uint16_t *dzp, float *tinv, float *part) {
+  constexpr int R = kGated ? 2 : 1, kSlice = kDzThreads * V * 8;
+  __shared__ __align__(16) float srinv[R][kSlice];
   __shared__ float red[kDzThreads / 32];
   __shared__ float peers[2][8];
   const int slices = gridDim.x, slice = blockIdx.x;  // a cluster is a row of the grid
   const int64_t F = kGated ? N / 2 : N;
   grid_launch_dependents();
   grid_dependency_wait();  // the row factors
-  int64_t f[kDzVecs];
+  int64_t f[V];
 #pragma unroll
-  for (int i = 0; i < kDzVecs; ++i) f[i] = ((int64_t)slice * kDzVecs * kDzThreads + i * kDzThreads + threadIdx.x) * 8;
-  for (int j = threadIdx.x; j < kDzSlice; j += kDzThreads) {
-    const int64_t n = (int64_t)slice * kDzSlice + j;
+  for (int i = 0; i < V; ++i) f[i] = (int64_t)slice * kSlice + (i * kDzThreads + (int)threadIdx.x) * 8;
+  for (int j = threadIdx.x; j < kSlice; j += kDzThreads) {
+    const int64_t n = (int64_t)slice * kSlice + j;
 #pragma unroll
     for (int h = 0; h < R; ++h) srinv[h][j] = n < F ? rinv[h * F + n] : 0.0f;
   }
   __syncthreads();
   if (slices > 1)  // every CTA of the cluster runs before one writes to another
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  uint4 raw[kDzVecs][1 + R];  // dY; Z (gated: G, U)
+  auto get = [&](const uint16_t *p, int64_t row, int64_t at, bool in) -> uint4 {  // elements at.. of a row; f .. F valid
+    if constexpr (kVec) {
+      return in ? *reinterpret_cast<const uint4 *>(p + row + at) : make_uint4(0, 0, 0, 0);
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t k = at % F + 2 * j;  // place in the row of F
+        const uint32_t lo = in && k < F ? p[row + at + 2 * j] : 0u, hi = in && k + 1 < F ? p[row + at + 2 * j + 1] : 0u;
+        w[j] = lo | hi << 16;
+      }
+      return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  };
+  uint4 raw[V][1 + R];  // dY; Z (gated: G, U)
   auto fetch = [&](int64_t m) {
 #pragma unroll
-    for (int i = 0; i < kDzVecs; ++i) {
+    for (int i = 0; i < V; ++i) {
       const bool in = m < M && f[i] < F;
-      raw[i][0] = in ? *reinterpret_cast<const uint4 *>(dY + m * F + f[i]) : make_uint4(0, 0, 0, 0);
-      raw[i][1] = in && Z ? *reinterpret_cast<const uint4 *>(Z + m * N + f[i]) : make_uint4(0, 0, 0, 0);
-      if constexpr (kGated) raw[i][2] = in ? *reinterpret_cast<const uint4 *>(Z + m * N + F + f[i]) : make_uint4(0, 0, 0, 0);
+      raw[i][0] = get(dY, m * F, f[i], in);
+      raw[i][1] = get(Z, m * N, f[i], in && Z);
+      if constexpr (kGated) raw[i][2] = get(Z, m * N, F + f[i], in);
     }
   };
   auto widen = [&](const uint4 &w, float (&v)[8]) {
     if (bf16) unpack8<true>(w, v);
     else unpack8<false>(w, v);
   };
-  float acc[kBias ? kDzVecs : 1][R][8] = {};
+  float acc[kBias ? V : 1][R][8] = {};
   fetch(blockIdx.y);
   int par = 0;
   for (int64_t m = blockIdx.y; m < M; m += gridDim.y, par ^= 1) {
-    float d[kDzVecs][R][8];
+    float d[V][R][8];
     float mx = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kDzVecs; ++i) {
-      float g[8], a[8], u[8];
+    for (int i = 0; i < V; ++i) {
+      float g[8], a[8], y[8], s[8];
       widen(raw[i][0], g);
       widen(raw[i][1], a);
-      if constexpr (kGated) widen(raw[i][R], u);
+      act_both8(a, Z ? act : (int)kActNone, y, s);
+      if constexpr (kGated) {
+        float u[8];
+        widen(raw[i][R], u);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float y = 0.0f, s = 1.0f;
-        if (Z) act_both(a[j], act, y, s);
-        if constexpr (kGated) {
-          d[i][0][j] = g[j] * u[j] * s;
-          d[i][R - 1][j] = g[j] * y;
-        } else {
-          d[i][0][j] = g[j] * s;
+        for (int j = 0; j < 8; ++j) {
+          d[i][0][j] = g[j] * u[j] * s[j];
+          d[i][R - 1][j] = g[j] * y[j];
         }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[i][0][j] = g[j] * s[j];
       }
 #pragma unroll
       for (int h = 0; h < R; ++h) {
@@ -303,33 +320,40 @@ __global__ void __launch_bounds__(kDzThreads, 2)
     }
     const float2 e = pow2_to(mx, 13);
     if (slice == 0 && threadIdx.x == 0) tinv[m] = e.y;
+    if (!kVec && slice == 0 && threadIdx.x < ld - N) dzp[m * ld + N + threadIdx.x] = 0;
 #pragma unroll
-    for (int i = 0; i < kDzVecs; ++i)
+    for (int i = 0; i < V; ++i)
       if (f[i] < F)
 #pragma unroll
         for (int h = 0; h < R; ++h) {
           const float(&x)[8] = d[i][h];
-          *reinterpret_cast<uint4 *>(dzp + m * N + h * F + f[i]) =
-              make_uint4(half2_bits(x[0] * e.x, x[1] * e.x), half2_bits(x[2] * e.x, x[3] * e.x),
-                         half2_bits(x[4] * e.x, x[5] * e.x), half2_bits(x[6] * e.x, x[7] * e.x));
+          const uint4 w = make_uint4(half2_bits(x[0] * e.x, x[1] * e.x), half2_bits(x[2] * e.x, x[3] * e.x),
+                                     half2_bits(x[4] * e.x, x[5] * e.x), half2_bits(x[6] * e.x, x[7] * e.x));
+          uint16_t *to = dzp + m * ld + h * F + f[i];
+          if constexpr (kVec) {
+            *reinterpret_cast<uint4 *>(to) = w;
+          } else {
+            const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (f[i] + j < F) to[j] = (uint16_t)(q[j >> 1] >> (16 * (j & 1)));
+          }
         }
   }
   if constexpr (kBias) {
 #pragma unroll
-    for (int i = 0; i < kDzVecs; ++i)
-      if (f[i] < F)
+    for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int h = 0; h < R; ++h) {
-          float4 *o = reinterpret_cast<float4 *>(part + (int64_t)blockIdx.y * N + h * F + f[i]);
-          o[0] = make_float4(acc[i][h][0], acc[i][h][1], acc[i][h][2], acc[i][h][3]);
-          o[1] = make_float4(acc[i][h][4], acc[i][h][5], acc[i][h][6], acc[i][h][7]);
-        }
+      for (int h = 0; h < R; ++h)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (f[i] + j < F) part[(int64_t)blockIdx.y * N + h * F + f[i] + j] = acc[i][h][j];
   }
   if (slices > 1)  // no CTA leaves while another may write to it
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// The same for rows that do not start on 16 bytes or are longer than a cluster's slices: one
+// The same for rows longer than a cluster's slices: one
 // token per block, in two passes (the second finds its inputs in L2); columns N.. up to
 // the row stride `ld` become 0.
 template <bool kGated, int kVec>
@@ -395,12 +419,20 @@ __global__ void __launch_bounds__(256)
 }
 
 __global__ void __launch_bounds__(256) fused_dbias_sum(const float *part, int ranges, int64_t N, float *dbias) {
-  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
+  __shared__ float sum[8][32];  // 32 columns, every eighth range to a warp
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t n = (int64_t)blockIdx.x * 32 + lane;
   float s = 0.0f;
+  if (n < N)
 #pragma unroll 8
-  for (int i = 0; i < ranges; ++i) s += part[i * N + n];
-  dbias[n] = s;
+    for (int i = w; i < ranges; i += 8) s += part[i * N + n];
+  sum[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && n < N) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += sum[i][lane];
+    dbias[n] = s;
+  }
 }
 
 // ------------------------------------------------------------------ launches
@@ -430,20 +462,22 @@ cudaError_t launch_fused_stage_x(const void *X, bool bf16, const float *awq_s, i
   return cudaGetLastError();
 }
 
-// Whether dz' is staged by clusters that hold a token between them.
-bool fused_dz_clusters(int64_t N, bool gated) {
-  const int64_t F = gated ? N / 2 : N;
-  return F % 8 == 0 && F <= 8 * kDzSlice;
+// Vectors per thread with which clusters of 8 reach over a token, 0 where they do not.
+int fused_dz_vecs(int64_t N, bool gated) {
+  const int64_t F = gated ? N / 2 : N, slice = kDzThreads * 8;
+  return F <= 8 * slice ? 1 : F <= 16 * slice ? 2 : 0;
 }
-// Its clusters: two CTAs per SM, at most one per token.
+// Clusters, at most: as many as the SMs hold at 3 (V = 1) or 2 CTAs each, one per token.
 int64_t fused_dz_grid(int64_t M, int64_t N, bool gated, int sm) {
-  const int64_t F = gated ? N / 2 : N, slices = (F + kDzSlice - 1) / kDzSlice, n = 2 * (int64_t)sm / slices;
+  const int v = fused_dz_vecs(N, gated);
+  const int64_t F = gated ? N / 2 : N, slice = kDzThreads * 8 * v, slices = (F + slice - 1) / slice;
+  const int64_t n = (v == 1 ? 3 : 2) * (int64_t)sm / slices;
   return M < n ? M : n < 1 ? 1 : n;
 }
 // Rows of dbias's partial sums: clusters, or ranges of tokens (about four blocks per SM, at
 // least 8 tokens each).
 int64_t fused_dbias_parts(int64_t M, int64_t N, bool gated, int sm) {
-  if (fused_dz_clusters(N, gated)) return fused_dz_grid(M, N, gated, sm);
+  if (fused_dz_vecs(N, gated)) return fused_dz_grid(M, N, gated, sm);
   const bool vec = (gated ? N / 2 : N) % 8 == 0;
   const int64_t cols = (N + (vec ? 256 : 32) - 1) / (vec ? 256 : 32);
   int64_t r = (600 + cols - 1) / cols;
@@ -454,8 +488,10 @@ int64_t fused_dbias_parts(int64_t M, int64_t N, bool gated, int sm) {
 cudaError_t launch_fused_stage_dz(const void *dY, const void *Z, int dtype, int act, bool gated, int64_t M, int64_t N,
                                   int64_t ld, const uint16_t *scales, const uint16_t *zeros, int64_t kg, uint16_t *dzp,
                                   float *tinv, float *rinv, uint32_t *tab, float *part, float *dbias, int sm,
-                                  cudaStream_t s) {
-  const bool vec = (gated ? N / 2 : N) % 8 == 0, clusters = fused_dz_clusters(N, gated);
+                                  int64_t *sums, cudaStream_t s) {
+  const bool vec = (gated ? N / 2 : N) % 8 == 0;
+  const int clusters = fused_dz_vecs(N, gated);
+  *sums = 0;
   int64_t parts = dbias ? fused_dbias_parts(M, N, gated, sm) : 0;
   if (dbias && !clusters) {
     const int64_t per = (M + parts - 1) / parts;
@@ -464,7 +500,7 @@ cudaError_t launch_fused_stage_dz(const void *dY, const void *Z, int dtype, int 
     auto k = gated ? (vec ? fused_dbias_part<true, 8> : fused_dbias_part<true, 1>)
                    : (vec ? fused_dbias_part<false, 8> : fused_dbias_part<false, 1>);
     k<<<grid, 256, 0, s>>>(dY, Z, dtype, act, M, N, per, part);
-    fused_dbias_sum<<<(unsigned)((N + 255) / 256), 256, 0, s>>>(part, (int)parts, N, dbias);
+    fused_dbias_sum<<<(unsigned)((N + 31) / 32), 256, 0, s>>>(part, (int)parts, N, dbias);
   }
   fused_prep<<<(unsigned)((N + kPrepRows - 1) / kPrepRows), kStageThreads, 0, s>>>(scales, zeros, kg, N, rinv, tab);
   cudaError_t e = cudaGetLastError();
@@ -474,9 +510,9 @@ cudaError_t launch_fused_stage_dz(const void *dY, const void *Z, int dtype, int 
                    : (vec ? fused_stage_dz_rows<false, 8> : fused_stage_dz_rows<false, 1>);
     return launch_pdl(k, dim3((unsigned)M), dim3(512), 0, s, dY, Z, dtype, act, N, ld, (const float *)rinv, dzp, tinv);
   }
-  const int64_t F = gated ? N / 2 : N;
+  const int64_t F = gated ? N / 2 : N, slice = kDzThreads * 8 * clusters;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((F + kDzSlice - 1) / kDzSlice), (unsigned)fused_dz_grid(M, N, gated, sm));
+  cfg.gridDim = dim3((unsigned)((F + slice - 1) / slice), 1);
   cfg.blockDim = dim3(kDzThreads);
   cfg.stream = s;
   cudaLaunchAttribute at[2];
@@ -487,16 +523,45 @@ cudaError_t launch_fused_stage_dz(const void *dY, const void *Z, int dtype, int 
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = cfg.gridDim.x > 1 ? 2 : 1;
-  auto k = gated ? (dbias ? fused_stage_dz<true, true> : fused_stage_dz<true, false>)
-                 : (dbias ? fused_stage_dz<false, true> : fused_stage_dz<false, false>);
+  auto pick = [&](auto g, auto b, auto v) {
+    constexpr bool G = decltype(g)::value, B = decltype(b)::value, C = decltype(v)::value;
+    return clusters == 1 ? fused_stage_dz<G, B, C, 1> : fused_stage_dz<G, B, C, 2>;
+  };
+  using T = std::true_type;
+  using U = std::false_type;
+  const bool bias = dbias != nullptr;
+  auto k = gated ? (bias ? (vec ? pick(T{}, T{}, T{}) : pick(T{}, T{}, U{})) : (vec ? pick(T{}, U{}, T{}) : pick(T{}, U{}, U{})))
+                 : (bias ? (vec ? pick(U{}, T{}, T{}) : pick(U{}, T{}, U{})) : (vec ? pick(U{}, U{}, T{}) : pick(U{}, U{}, U{})));
+  // No more clusters than run at a time (a few left over would take as long again): what the
+  // device holds of this kernel and cluster size, asked once.
+  static std::atomic<int> known[kAttrDevices][16][8];
+  int dev = 0, most = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  std::atomic<int> *kn = dev >= 0 && dev < kAttrDevices
+                             ? &known[dev][8 * gated + 4 * bias + 2 * vec + (clusters == 1)][cfg.gridDim.x - 1] : nullptr;
+  if (kn) most = kn->load(std::memory_order_relaxed);
+  if (most == 0) {
+    cudaLaunchConfig_t q = cfg;
+    q.gridDim.y = 1024;
+    q.attrs = at + 1;
+    q.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&most, k, &q) != cudaSuccess || most < 1) {
+      cudaGetLastError();
+      most = sm / (int)cfg.gridDim.x > 0 ? sm / (int)cfg.gridDim.x : 1;
+    }
+    if (kn) kn->store(most, std::memory_order_relaxed);
+  }
+  const int64_t want = fused_dz_grid(M, N, gated, sm);
+  *sums = want < most ? want : most;
+  cfg.gridDim.y = (unsigned)*sums;
   return cudaLaunchKernelEx(&cfg, k, static_cast<const uint16_t *>(dY), static_cast<const uint16_t *>(Z), dtype == 2 ? 1 : 0,
-                            act, M, N, (const float *)rinv, dzp, tinv, part);
+                            act, M, N, ld, (const float *)rinv, dzp, tinv, part);
 }
 
 // Behind the product (which does not wait for it): dbias from the clusters' sums.
-cudaError_t launch_fused_dbias_sum(int64_t M, int64_t N, bool gated, const float *part, float *dbias, int sm, cudaStream_t s) {
-  if (!fused_dz_clusters(N, gated)) return cudaSuccess;  // summed already
-  fused_dbias_sum<<<(unsigned)((N + 255) / 256), 256, 0, s>>>(part, (int)fused_dbias_parts(M, N, gated, sm), N, dbias);
+cudaError_t launch_fused_dbias_sum(int64_t N, int64_t sums, const float *part, float *dbias, cudaStream_t s) {
+  if (sums == 0) return cudaSuccess;  // summed already
+  fused_dbias_sum<<<(unsigned)((N + 31) / 32), 256, 0, s>>>(part, (int)sums, N, dbias);
   return cudaGetLastError();
 }
 

@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
 }
 
 // Sums the partial tiles of the tiles cut along the contraction, in order, and runs the
-// epilogue: one block per tile and 8 (gated: 16) tokens, 4 outputs per thread.
+// epilogue: 4 outputs per thread, 8 (gated: 16) tokens per block at a time.
 template <int kMode>
 __global__ void __launch_bounds__(256) fused_finish(const FusedTcParams p) {
   using namespace ftc;
@@ -724,31 +724,37 @@ __global__ void __launch_bounds__(256) fused_finish(const FusedTcParams p) {
   const bool second = begin(c0) < u0;  // pair c0 began in the tile before
   int row, tok;
   tile_at(p, p.full + t, rank, row, tok);
-  const int tt = blockIdx.y * kTok + threadIdx.x / kPer, col = 4 * (threadIdx.x % kPer);
-  const int64_t m = (int64_t)tok * p.bn + tt;
+  const int col = 4 * (threadIdx.x % kPer);
   const int64_t n = kMode == kGated ? (int64_t)row * 64 + col : (int64_t)row * 128 + col;
-  if (tt >= p.bn || m >= e.M || n >= e.N) return;
-  float4 v = make_float4(0, 0, 0, 0), w = v;
-  auto add = [](float4 &a, const float4 &x) { a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w; };
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const int64_t slot = 2 * c + (c == c0 && second ? 1 : 0);
-    const float *src = p.part + ((slot * 2 + rank) * p.bn + tt) * 128 + col;
-    add(v, *reinterpret_cast<const float4 *>(src));
-    if (kMode == kGated) add(w, *reinterpret_cast<const float4 *>(src + 64));
-  }
-  const float inv = e.tinv[m];
-  ColK k;
-  float z[4];
+  if (n >= e.N) return;
+  ColK k, ku;
   k.load(e, kMode == kGrad, n, n, e.N);
-  k.scale(v, inv, z);
-  if (kMode == kGated) {
-    float u[4];
-    k.load(e, false, e.N + n, n, e.N);
-    k.scale(w, inv, u);
-    finish_gated(e, m, n, z, u);
-  } else {
-    finish_linear(e, m, n, z, false, make_uint2(0, 0));
+  if (kMode == kGated) ku.load(e, false, e.N + n, n, e.N);
+  const float *first = p.part + (((int64_t)2 * c0 + (second ? 1 : 0)) * 2 + rank) * p.bn * 128 + col;
+  const float *rest = p.part + ((int64_t)4 * (c0 + 1) + rank) * p.bn * 128 + col;  // then every 4 bn rows
+  auto add = [](float4 &a, const float4 &x) { a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w; };
+  const int lim = (int)min((int64_t)p.bn, e.M - (int64_t)tok * p.bn);
+#pragma unroll 2
+  for (int tt = blockIdx.y * kTok + threadIdx.x / kPer; tt < lim; tt += gridDim.y * kTok) {
+    const int64_t m = (int64_t)tok * p.bn + tt;
+    const float *src = first + tt * 128, *more = rest + tt * 128;
+    float4 v = *reinterpret_cast<const float4 *>(src), w = make_float4(0, 0, 0, 0);
+    if (kMode == kGated) w = *reinterpret_cast<const float4 *>(src + 64);
+#pragma unroll 2
+    for (int c = c0 + 1; c <= c1; ++c, more += (int64_t)4 * p.bn * 128) {
+      add(v, *reinterpret_cast<const float4 *>(more));
+      if (kMode == kGated) add(w, *reinterpret_cast<const float4 *>(more + 64));
+    }
+    const float inv = e.tinv[m];
+    float z[4];
+    k.scale(v, inv, z);
+    if (kMode == kGated) {
+      float u[4];
+      ku.scale(w, inv, u);
+      finish_gated(e, m, n, z, u);
+    } else {
+      finish_linear(e, m, n, z, false, make_uint2(0, 0));
+    }
   }
 }
 
@@ -775,9 +781,11 @@ cudaError_t launch_fused_tc_mode(const CUtensorMap &tmX, const CUtensorMap &tmP,
   cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, fused_tc_kernel<kMode>, tmX, tmP, p);
   if (e != cudaSuccess || p.full == p.tiles) return e;
-  const int tok = kMode == kGated ? 16 : 8;
-  return launch_pdl(fused_finish<kMode>, dim3((unsigned)(2 * (p.tiles - p.full)), (unsigned)((p.bn + tok - 1) / tok)), dim3(256),
-                    (size_t)0, s, p);
+  // about six blocks per SM, each at least one step of 8 (16) tokens
+  const int tok = kMode == kGated ? 16 : 8, cut = 2 * (p.tiles - p.full), steps = (p.bn + tok - 1) / tok;
+  int y = (12 * pairs + cut - 1) / cut;
+  y = y > steps ? steps : y;
+  return launch_pdl(fused_finish<kMode>, dim3((unsigned)cut, (unsigned)y), dim3(256), (size_t)0, s, p);
 }
 
 cudaError_t launch_fused_tc(int mode, const CUtensorMap &tmX, const CUtensorMap &tmP, const FusedTcParams &p, int pairs,
