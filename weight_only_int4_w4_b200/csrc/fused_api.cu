@@ -170,10 +170,6 @@ FusedRoute fused_route(const FusedCall &c) {
 w4_status fused_check(const FusedCall &c) {
   w4_status st = check_shape(c.M, c.N, c.K, c.group);
   if (st != W4_OK) return st;
-  FusedPlan plan;
-  if (!fused_plan(c.M, c.N, c.K, c.gated, c.grad, sm_count_or_b200(), plan))
-    return fail(W4_ERR_INVALID_ARG, "M=%lld N=%lld K=%lld: too many tiles for one launch", (long long)c.M, (long long)c.N,
-                (long long)c.K);
   if (c.K % 64 != 0) return fail(W4_ERR_UNSUPPORTED, "K=%lld must be a multiple of 64", (long long)c.K);
   if (c.x_dtype != W4_F16 && c.x_dtype != W4_BF16)
     return fail(W4_ERR_UNSUPPORTED, "%s dtype must be F16 or BF16", c.grad ? "gradient" : "activation");
@@ -211,8 +207,12 @@ w4_status fused_check(const FusedCall &c) {
   for (int i = 0; i < 8; ++i)
     if (overlap(c.workspace, c.workspace_bytes, ins[i].p, ins[i].n))
       return fail(W4_ERR_INVALID_ARG, "the workspace overlaps an input");
-  const size_t need = fused_route(c) == kRouteDecode ? 0 : fused_ws_bytes(c.M, c.N, c.K, c.gated, c.grad);
-  if (need > 0 && (!c.workspace || c.workspace_bytes < need))
+  if (fused_route(c) == kRouteDecode) return W4_OK;  // takes no workspace
+  const size_t need = fused_ws_bytes(c.M, c.N, c.K, c.gated, c.grad);
+  if (need == 0)
+    return fail(W4_ERR_INVALID_ARG, "M=%lld N=%lld K=%lld: too many tiles for one launch", (long long)c.M, (long long)c.N,
+                (long long)c.K);
+  if (!c.workspace || c.workspace_bytes < need)
     return fail(W4_ERR_INVALID_ARG, "workspace too small: need %zu bytes, got %zu", need,
                 c.workspace ? c.workspace_bytes : (size_t)0);
   return W4_OK;

@@ -401,43 +401,43 @@ def _bad(name, what):
 
 
 def _fused_layer(name, X, packed, scales, zeros, awq_s, group):
-    """The checks that every fused call shares; returns (device, M, N, K)."""
-    if not (X.is_cuda and X.dim() == 2 and X.dtype in _X_DT and X.is_contiguous()):
+    """The checks that every fused call shares; returns (device index, M, N, K)."""
+    dev = X.get_device()
+    if dev < 0 or X.dim() != 2 or X.dtype not in _X_DT or not X.is_contiguous():
         _bad(name, "the activations or gradients are a contiguous 2-D CUDA tensor in fp16 or bf16")
-    dev = X.device
-    if not (packed.dtype == torch.uint8 and packed.dim() == 2 and packed.is_contiguous() and packed.device == dev):
+    if packed.dtype is not torch.uint8 or packed.dim() != 2 or not packed.is_contiguous() or packed.get_device() != dev:
         _bad(name, "packed is a contiguous uint8 [N, K/2] tensor on the activations' device")
     if type(group) is not int or group < 1:
         _bad(name, "group is a positive number")
     N, K = packed.shape
     K *= 2
     shape = (N, K // group)
-    if not (scales.dtype == zeros.dtype == torch.float16 and scales.shape == zeros.shape == shape and
-            scales.is_contiguous() and zeros.is_contiguous() and scales.device == zeros.device == dev):
-        _bad(name, f"scales and zeros are contiguous fp16 tensors of shape {shape} on {dev}")
+    for t in (scales, zeros):
+        if t.dtype is not torch.float16 or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+            _bad(name, f"scales and zeros are contiguous fp16 tensors of shape {shape} on the activations' device")
     if awq_s is not None:
         _vector(name, "awq_s", awq_s, K, dev)
     return dev, X.shape[0], N, K
 
 
 def _vector(name, what, t, n, dev):
-    if not (t.dtype == torch.float32 and t.shape == (n,) and t.is_contiguous() and t.device == dev):
-        _bad(name, f"{what} is a contiguous fp32 tensor of {n} elements on {dev}")
+    if t.dtype is not torch.float32 or t.shape != (n,) or not t.is_contiguous() or t.get_device() != dev:
+        _bad(name, f"{what} is a contiguous fp32 tensor of {n} elements on the activations' device")
 
 
 def _matrix(name, what, t, M, N, dtype, dev):
-    if not (t.dtype == dtype and t.shape == (M, N) and t.is_contiguous() and t.device == dev):
-        _bad(name, f"{what} is a contiguous {dtype} tensor of shape [{M}, {N}] on {dev}")
+    if t.dtype is not dtype or t.shape != (M, N) or not t.is_contiguous() or t.get_device() != dev:
+        _bad(name, f"{what} is a contiguous {dtype} tensor of shape [{M}, {N}] on the activations' device")
 
 
-def _output(name, out, M, N, out_dtype, like):
+def _output(name, out, M, N, out_dtype, like, dev):
     if out is None:
         if out_dtype is not None and out_dtype not in _DT:
             _bad(name, "the output is fp32, fp16 or bf16")
         return like.new_empty((M, N), dtype=out_dtype)
     if out.dtype not in _DT or out_dtype not in (None, out.dtype):
         _bad(name, "out is fp32, fp16 or bf16, and of out_dtype if that is given")
-    _matrix(name, "out", out, M, N, out.dtype, like.device)
+    _matrix(name, "out", out, M, N, out.dtype, dev)
     return out
 
 
@@ -447,20 +447,19 @@ def _act(name, act):
 
 
 def _fused_call(name, fn, size_fn, sizes, dev, ws, stream, args):
-    """Makes the C call on `dev`: args and then the workspace and stream."""
-    idx = dev.index
-    if torch._C._cuda_getDevice() != idx:
+    """Makes the C call on device `dev`: args and then the workspace and stream."""
+    if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return _fused_call(name, fn, size_fn, sizes, dev, ws, stream, args)
-    raw = _raw_stream(idx) if stream is None else stream.cuda_stream
+    raw = _raw_stream(dev) if stream is None else stream.cuda_stream
     if ws is None:
         if size_fn is not None:
             need = size_fn(*sizes)
             ws = _fused_workspace(need, dev, raw, stream) if need else None
-    elif not (ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev):
-        _bad(name, f"ws is a contiguous uint8 tensor on {dev}")
-    st = fn(*args, ws.data_ptr() if ws is not None else 0, ws.numel() if ws is not None else 0, raw)
-    if st != W4_OK:
+    elif ws.dtype is not torch.uint8 or not ws.is_contiguous() or ws.get_device() != dev:
+        _bad(name, "ws is a contiguous uint8 tensor on the activations' device")
+    st = fn(*args, 0, 0, raw) if ws is None else fn(*args, ws.data_ptr(), ws.numel(), raw)
+    if st:
         raise W4Error(st, name)
 
 
@@ -479,7 +478,7 @@ def w4a16_linear(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, ze
     a = _act(name, act)
     if bias is not None:
         _vector(name, "bias", bias, N, dev)
-    Y = _output(name, out, M, N, out_dtype, X)
+    Y = _output(name, out, M, N, out_dtype, X, dev)
     if residual is not None:
         _matrix(name, "residual", residual, M, N, Y.dtype, dev)
     Z = X.new_empty((M, N)) if save_preact else None
@@ -509,7 +508,7 @@ def w4a16_gated(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zer
     if bias is not None:
         _vector(name, "bias", bias, N, dev)
     F = N // 2
-    H = _output(name, out, M, F, out_dtype, X)
+    H = _output(name, out, M, F, out_dtype, X, dev)
     Z = X.new_empty((M, N)) if save_preact else None
     decode = M <= _DECODE_TOKENS and group == GROUP
     _fused_call(name, _lib.w4a16_gated, None if decode else _lib.w4a16_gated_workspace_size, (M, F, K), dev, ws, stream,
@@ -551,7 +550,7 @@ def _grad(name, gated, fn, size_fn, dY, packed, scales, zeros, awq_s, preact, ac
     a = _act(name, act)
     if preact is not None:
         _matrix(name, "preact", preact, M, N, dY.dtype, dev)
-    dX = _output(name, out, M, K, out_dtype, dY)
+    dX = _output(name, out, M, K, out_dtype, dY, dev)
     db = dY.new_empty(N, dtype=torch.float32) if dbias else None
     _fused_call(name, fn, size_fn, (M, width, K), dev, ws, stream,
                 (dY.data_ptr(), _X_DT[dY.dtype], M, width, K, group, packed.data_ptr(), scales.data_ptr(),
