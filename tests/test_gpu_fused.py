@@ -223,6 +223,18 @@ def test_gated_grad(w4, i, shape):
     check_grad(w4, L, dH, Z, act, True, group, i % 2 == 1, (dt, torch.float32)[i % 2], f"gated_grad {shape} {act}")
 
 
+@pytest.mark.parametrize("gated,N", [(False, 16392), (False, 33001), (True, 2 * 16400), (True, 2 * 20003), (False, 65600),
+                                     (False, 65537), (True, 2 * 65543)])
+def test_grad_of_wide_layers(w4, gated, N):
+    """Widths of every staging path: clusters of CTAs with one and two vectors a thread, rows
+    on 16 bytes or not, and rows longer than a cluster's slices."""
+    M, K = 21, 64
+    L = Layer(w4, N, K, group=64, seed=7)
+    dY = (L.randn(M, N // 2 if gated else N) * 1e-3).to(torch.bfloat16)
+    Z = (L.randn(M, N) * 1.4).to(torch.bfloat16)
+    check_grad(w4, L, dY, Z, "silu", gated, 64, True, torch.bfloat16, f"wide gradient {gated} {N}")
+
+
 @pytest.mark.parametrize("gated", [False, True])
 def test_gradient_against_differences(w4, gated):
     """<dX, V> against the central difference of f(X) = <dY, layer(X)> along V, in 64 bits.

@@ -200,19 +200,21 @@ __device__ __forceinline__ void dz_at(const void *dY, const void *Z, int dtype, 
 }
 
 // dz' = fp16(dZ / r[n] * e), natural order, and 1 / e.  A cluster of CTAs takes tokens in turn,
-// each CTA the same 256 V vectors of 8 outputs f (of a gated call: rows f and F + f, which
+// each CTA the same vectors of 8 outputs f (V to a thread) (of a gated call: rows f and F + f, which
 // share their inputs) of every token: dZ stays in registers while the CTAs exchange the
 // token's largest value, the next token's inputs are on their way meanwhile, and dbias's
 // sums over the cluster's tokens, to part [cluster][N], cost nothing but additions.
 // V = 1 where a cluster of 8 reaches over F with it (more CTAs then hide each other's
-// exchanges), else 2.  kVec: rows start on 16 bytes; else elements one at a time.
-constexpr int kDzThreads = 256;
+// exchanges), else 2, with 512 threads where one row factor per column leaves the shared
+// memory for it.  kVec: rows start on 16 bytes; else elements one at a time.
+__host__ __device__ constexpr int dz_threads(bool gated, int v) { return v == 1 || gated ? 256 : 512; }
+__host__ __device__ constexpr int dz_per_sm(bool gated, int v) { return v == 1 ? 3 : gated ? 2 : 1; }
 
 template <bool kGated, bool kBias, bool kVec, int V>
-__global__ void __launch_bounds__(kDzThreads, V == 1 ? 3 : 2)
+__global__ void __launch_bounds__(dz_threads(kGated, V), dz_per_sm(kGated, V))
     fused_stage_dz(const uint16_t *dY, const uint16_t *Z, int bf16, int act, int64_t M, int64_t N, int64_t ld,
                    const float *rinv, uint16_t *dzp, float *tinv, float *part) {
-  constexpr int R = kGated ? 2 : 1, kSlice = kDzThreads * V * 8;
+  constexpr int R = kGated ? 2 : 1, kDzThreads = dz_threads(kGated, V), kSlice = kDzThreads * V * 8;
   __shared__ __align__(16) float srinv[R][kSlice];
   __shared__ float red[kDzThreads / 32];
   __shared__ float peers[2][8];
@@ -464,14 +466,14 @@ cudaError_t launch_fused_stage_x(const void *X, bool bf16, const float *awq_s, i
 
 // Vectors per thread with which clusters of 8 reach over a token, 0 where they do not.
 int fused_dz_vecs(int64_t N, bool gated) {
-  const int64_t F = gated ? N / 2 : N, slice = kDzThreads * 8;
-  return F <= 8 * slice ? 1 : F <= 16 * slice ? 2 : 0;
+  const int64_t F = gated ? N / 2 : N;
+  return F <= 8 * 8 * dz_threads(gated, 1) ? 1 : F <= 8 * 16 * dz_threads(gated, 2) ? 2 : 0;
 }
-// Clusters, at most: as many as the SMs hold at 3 (V = 1) or 2 CTAs each, one per token.
+// Clusters, at most: as many as the SMs hold, one per token.
 int64_t fused_dz_grid(int64_t M, int64_t N, bool gated, int sm) {
   const int v = fused_dz_vecs(N, gated);
-  const int64_t F = gated ? N / 2 : N, slice = kDzThreads * 8 * v, slices = (F + slice - 1) / slice;
-  const int64_t n = (v == 1 ? 3 : 2) * (int64_t)sm / slices;
+  const int64_t F = gated ? N / 2 : N, slice = dz_threads(gated, v) * 8 * v, slices = (F + slice - 1) / slice;
+  const int64_t n = dz_per_sm(gated, v) * (int64_t)sm / slices;
   return M < n ? M : n < 1 ? 1 : n;
 }
 // Rows of dbias's partial sums: clusters, or ranges of tokens (about four blocks per SM, at
@@ -510,10 +512,10 @@ cudaError_t launch_fused_stage_dz(const void *dY, const void *Z, int dtype, int 
                    : (vec ? fused_stage_dz_rows<false, 8> : fused_stage_dz_rows<false, 1>);
     return launch_pdl(k, dim3((unsigned)M), dim3(512), 0, s, dY, Z, dtype, act, N, ld, (const float *)rinv, dzp, tinv);
   }
-  const int64_t F = gated ? N / 2 : N, slice = kDzThreads * 8 * clusters;
+  const int64_t F = gated ? N / 2 : N, slice = dz_threads(gated, clusters) * 8 * clusters;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((F + slice - 1) / slice), 1);
-  cfg.blockDim = dim3(kDzThreads);
+  cfg.blockDim = dim3(dz_threads(gated, clusters));
   cfg.stream = s;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

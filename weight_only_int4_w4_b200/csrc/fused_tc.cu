@@ -283,22 +283,31 @@ __device__ __forceinline__ uint32_t narrow2(float a, float b, int dtype) {
   return dtype == 2 ? *reinterpret_cast<const uint32_t *>(&x) : half2_bits(a, b);
 }
 
-// One value at a time: rows that do not start on a vector.
-__device__ __noinline__ void put4_slow(void *p, int dtype, int64_t at, int count, float a, float b, float c, float d) {
-  const float v[4] = {a, b, c, d};
-#pragma unroll 1
-  for (int j = 0; j < count; ++j) store_from_float(p, dtype, at + j, j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[2] : v[3]);
-}
-
-// Stores v at columns n.. of a row that starts at element `row`; n + j < lim.
+// Stores v at columns n.. of a row that starts at element `row`; n + j < lim (a multiple of 4
+// where rows start on vectors).
 __device__ __forceinline__ void put4(void *p, int dtype, int64_t row, int64_t n, int64_t lim, bool vec, const float (&v)[4]) {
-  if (!vec) {  // else lim is a multiple of 4
-    put4_slow(p, dtype, row + n, (int)min((int64_t)4, lim - n), v[0], v[1], v[2], v[3]);
-  } else if (dtype != 0) {
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + row + n) =
-        make_uint2(narrow2(v[0], v[1], dtype), narrow2(v[2], v[3], dtype));
+  const int in = (int)min((int64_t)4, lim - n);
+  if (dtype != 0) {
+    const uint32_t a = narrow2(v[0], v[1], dtype), b = narrow2(v[2], v[3], dtype);
+    uint16_t *q = static_cast<uint16_t *>(p) + row + n;
+    if (vec) {
+      *reinterpret_cast<uint2 *>(q) = make_uint2(a, b);
+    } else {
+      q[0] = (uint16_t)a;
+      if (in > 1) q[1] = (uint16_t)(a >> 16);
+      if (in > 2) q[2] = (uint16_t)b;
+      if (in > 3) q[3] = (uint16_t)(b >> 16);
+    }
   } else {
-    *reinterpret_cast<float4 *>(static_cast<float *>(p) + row + n) = make_float4(v[0], v[1], v[2], v[3]);
+    float *q = static_cast<float *>(p) + row + n;
+    if (vec) {
+      *reinterpret_cast<float4 *>(q) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      q[0] = v[0];
+      if (in > 1) q[1] = v[1];
+      if (in > 2) q[2] = v[2];
+      if (in > 3) q[3] = v[3];
+    }
   }
 }
 
@@ -323,9 +332,13 @@ struct ColK {
   }
 };
 
-// The residual's four values at (m, n), as they lie (16 bits, aligned) or nothing.
+// The residual's four values at (m, n), as they lie (16 bits); 0 behind the last column.
 __device__ __forceinline__ uint2 residual4(const FusedEpi &e, int64_t m, int64_t n) {
-  return *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(e.residual) + m * e.N + n);
+  const uint16_t *q = static_cast<const uint16_t *>(e.residual) + m * e.N + n;
+  if (e.vec) return *reinterpret_cast<const uint2 *>(q);
+  const int in = (int)min((int64_t)4, e.N - n);
+  const uint32_t a = q[0], b = in > 1 ? q[1] : 0u, c = in > 2 ? q[2] : 0u, d = in > 3 ? q[3] : 0u;
+  return make_uint2(a | b << 16, c | d << 16);
 }
 
 // `res`: the residual's values where `have`, else they are read here.
@@ -338,7 +351,7 @@ __device__ __forceinline__ void finish_linear(const FusedEpi &e, int64_t m, int6
     widen4(res, e.y_dtype, a);
 #pragma unroll
     for (int j = 0; j < 4; ++j) z[j] += a[j];
-  } else if (e.residual) {  // fp32, or rows that do not start on a vector
+  } else if (e.residual) {  // fp32
 #pragma unroll 1
     for (int j = 0; j < 4; ++j) {
       z[0] += n + j < e.N ? load_as_float(e.residual, e.y_dtype, row + n + j) : 0.0f;
@@ -622,7 +635,7 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
         c0.load(e, kIsGrad, n, n, e.N);
         if (kMode == kGated) c1.load(e, false, e.N + n, n, e.N);
       }
-      const bool ahead = kMode == kLinear && slot < 0 && e.residual && e.vec && e.y_dtype != 0 && n < e.N;
+      const bool ahead = kMode == kLinear && slot < 0 && e.residual && e.y_dtype != 0 && n < e.N;
       if (!vote_epilogue(mbar_wait(&dfull[d], dph, kErrTimeoutEpilogue))) break;
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(d * p.bn);
@@ -753,7 +766,8 @@ __global__ void __launch_bounds__(256) fused_finish(const FusedTcParams p) {
       ku.scale(w, inv, u);
       finish_gated(e, m, n, z, u);
     } else {
-      finish_linear(e, m, n, z, false, make_uint2(0, 0));
+      const bool have = e.residual && e.y_dtype != 0;
+      finish_linear(e, m, n, z, have, have ? residual4(e, m, n) : make_uint2(0, 0));
     }
   }
 }
