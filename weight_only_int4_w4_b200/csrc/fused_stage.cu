@@ -222,9 +222,15 @@ __global__ void __launch_bounds__(dz_threads(kGated, V), dz_per_sm(kGated, V))
   const int64_t F = kGated ? N / 2 : N;
   grid_launch_dependents();
   grid_dependency_wait();  // the row factors
+  // A thread's outputs: at(i, j) of the slice, its 8 V values V vectors where rows start on
+  // 16 bytes; else a warp's 32 threads read 32 neighbours.
+  auto at = [&](int i, int j) {
+    return kVec ? (i * kDzThreads + (int)threadIdx.x) * 8 + j : (i * 8 + j) * kDzThreads + (int)threadIdx.x;
+  };
+  const int64_t first = (int64_t)slice * kSlice;
   int64_t f[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) f[i] = (int64_t)slice * kSlice + (i * kDzThreads + (int)threadIdx.x) * 8;
+  for (int i = 0; i < V; ++i) f[i] = first + at(i, 0);
   for (int j = threadIdx.x; j < kSlice; j += kDzThreads) {
     const int64_t n = (int64_t)slice * kSlice + j;
 #pragma unroll
@@ -233,28 +239,27 @@ __global__ void __launch_bounds__(dz_threads(kGated, V), dz_per_sm(kGated, V))
   __syncthreads();
   if (slices > 1)  // every CTA of the cluster runs before one writes to another
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  auto get = [&](const uint16_t *p, int64_t row, int64_t at, bool in) -> uint4 {  // elements at.. of a row; f .. F valid
+  // The thread's values i of a row.  Behind F: 0, or where elements are read one at a time the
+  // last one again, whose row factor is 0 (reads under a condition are not moved up, and each
+  // pair waits for the one before: 2,800 instead of 990 us at M = 7355, N = 37373).
+  auto get = [&](const uint16_t *row, int i) -> uint4 {
     if constexpr (kVec) {
-      return in ? *reinterpret_cast<const uint4 *>(p + row + at) : make_uint4(0, 0, 0, 0);
+      return f[i] < F ? *reinterpret_cast<const uint4 *>(row + f[i]) : make_uint4(0, 0, 0, 0);
     } else {
-      uint32_t w[4];
+      uint32_t w[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t k = at % F + 2 * j;  // place in the row of F
-        const uint32_t lo = in && k < F ? p[row + at + 2 * j] : 0u, hi = in && k + 1 < F ? p[row + at + 2 * j + 1] : 0u;
-        w[j] = lo | hi << 16;
-      }
-      return make_uint4(w[0], w[1], w[2], w[3]);
+      for (int j = 0; j < 8; ++j) w[j] = row[min(first + at(i, j), F - 1)];
+      return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
     }
   };
   uint4 raw[V][1 + R];  // dY; Z (gated: G, U)
   auto fetch = [&](int64_t m) {
+    m = min(m, M - 1);  // (the last fetch is not used)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const bool in = m < M && f[i] < F;
-      raw[i][0] = get(dY, m * F, f[i], in);
-      raw[i][1] = get(Z, m * N, f[i], in && Z);
-      if constexpr (kGated) raw[i][2] = get(Z, m * N, F + f[i], in);
+      raw[i][0] = get(dY + m * F, i);
+      raw[i][1] = get(Z ? Z + m * N : dY + m * F, i);  // (unused without Z)
+      if constexpr (kGated) raw[i][2] = get(Z + m * N + F, i);
     }
   };
   auto widen = [&](const uint4 &w, float (&v)[8]) {
@@ -287,11 +292,16 @@ __global__ void __launch_bounds__(dz_threads(kGated, V), dz_per_sm(kGated, V))
       }
 #pragma unroll
       for (int h = 0; h < R; ++h) {
-        const float *q = srinv[h] + (i * kDzThreads + threadIdx.x) * 8;
 #pragma unroll
         for (int j = 0; j < 8; j += 4) {
-          const float4 x = *reinterpret_cast<const float4 *>(q + j);
-          const float r4[4] = {x.x, x.y, x.z, x.w};
+          float r4[4];
+          if constexpr (kVec) {
+            const float4 x = *reinterpret_cast<const float4 *>(srinv[h] + at(i, j));
+            r4[0] = x.x, r4[1] = x.y, r4[2] = x.z, r4[3] = x.w;
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) r4[k] = srinv[h][at(i, j + k)];
+          }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if constexpr (kBias) acc[i][h][j + k] += d[i][h][j + k];
@@ -331,14 +341,14 @@ __global__ void __launch_bounds__(dz_threads(kGated, V), dz_per_sm(kGated, V))
           const float(&x)[8] = d[i][h];
           const uint4 w = make_uint4(half2_bits(x[0] * e.x, x[1] * e.x), half2_bits(x[2] * e.x, x[3] * e.x),
                                      half2_bits(x[4] * e.x, x[5] * e.x), half2_bits(x[6] * e.x, x[7] * e.x));
-          uint16_t *to = dzp + m * ld + h * F + f[i];
+          uint16_t *to = dzp + m * ld + h * F + first;
           if constexpr (kVec) {
-            *reinterpret_cast<uint4 *>(to) = w;
+            *reinterpret_cast<uint4 *>(to + at(i, 0)) = w;
           } else {
             const uint32_t q[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              if (f[i] + j < F) to[j] = (uint16_t)(q[j >> 1] >> (16 * (j & 1)));
+              if (first + at(i, j) < F) to[at(i, j)] = (uint16_t)(q[j >> 1] >> (16 * (j & 1)));
           }
         }
   }
@@ -349,7 +359,7 @@ __global__ void __launch_bounds__(dz_threads(kGated, V), dz_per_sm(kGated, V))
       for (int h = 0; h < R; ++h)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (f[i] + j < F) part[(int64_t)blockIdx.y * N + h * F + f[i] + j] = acc[i][h][j];
+          if (first + at(i, j) < F) part[(int64_t)blockIdx.y * N + h * F + first + at(i, j)] = acc[i][h][j];
   }
   if (slices > 1)  // no CTA leaves while another may write to it
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -556,6 +566,10 @@ cudaError_t launch_fused_stage_dz(const void *dY, const void *Z, int dtype, int 
   const int64_t want = fused_dz_grid(M, N, gated, sm);
   *sums = want < most ? want : most;
   cfg.gridDim.y = (unsigned)*sums;
+  // A grid that fills the device starts behind the row factors, not among their blocks: those
+  // keep clusters from packing, and one left over takes as long again (twice the time at M = 7355,
+  // N = 37373, in every second call).
+  at[0].val.programmaticStreamSerializationAllowed = *sums <= most / 2;
   return cudaLaunchKernelEx(&cfg, k, static_cast<const uint16_t *>(dY), static_cast<const uint16_t *>(Z), dtype == 2 ? 1 : 0,
                             act, M, N, ld, (const float *)rinv, dzp, tinv, part);
 }
