@@ -453,6 +453,99 @@ def test_offsets_past_32_bits(w4):
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("M", [3, 20, 90])
+def test_negative_scales(w4, M):
+    """Scales of either sign, and rows that have only negative ones: as precise as positive ones."""
+    N, K = 264, 768
+    L = Layer(w4, N, K)
+    p, sc, z = L.w
+    sign = torch.ones_like(sc)
+    sign[::2] = -1
+    sign[1::4, ::2] = -1
+    L.w = (p, sc * sign, z)
+    L.What = L.What * sign.double().repeat_interleave(128, 1)
+    X = L.randn(M, K).to(torch.float16)
+    Zr = L.z64(X, None)
+    Y = w4.w4a16_linear(X, *L.w, out_dtype=torch.float32)
+    check(Y, Zr, L.z_tol(X, Zr, False), U, f"negative scales M={M}")
+    dY = L.randn(M, N).to(torch.float16)
+    check_grad(w4, L, dY, None, "none", False, 128, True, torch.float32, f"negative scales, gradient M={M}")
+
+
+def test_weights_past_32_bits(w4):
+    """More than 2^31 bytes of codes (and 2^32 weights): outputs of the first and last rows, and
+    the gradient that comes from them."""
+    N, K = 150016, 32768
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    p = torch.randint(0, 256, (N, K // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    sc = (torch.rand((N, K // 128), generator=gen, device="cuda") * 0.01 + 0.001).half()
+    z = torch.randint(0, 16, (N, K // 128), generator=gen, device="cuda").half()
+    rows = torch.tensor([0, 1, N // 2 - 1, N // 2, 131071, 131072, N - 2, N - 1], device="cuda")
+    q = torch.stack([p[rows] & 15, p[rows] >> 4], 2).view(len(rows), K // 128, 128).double()
+    What = ((q - z[rows].double()[:, :, None]) * sc[rows].double()[:, :, None]).view(len(rows), K)
+    big = (15 * sc[rows].double()).repeat_interleave(128, 1)
+    for M in (2, 20, 70):
+        X = torch.randn((M, K), generator=gen, device="cuda").to(torch.bfloat16)
+        ref = X.double() @ What.t()
+        tol = U * (X.double().abs() @ What.abs().t()) + K * 2.0 ** -23 * (X.double().abs() @ big.t())
+        Y = w4.w4a16_linear(X, p, sc, z, out_dtype=torch.float32)
+        check(Y[:, rows], ref, tol, U, f"weights past 32 bits M={M}")
+        dY = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
+        dY[:, rows] = torch.randn((M, len(rows)), generator=gen, device="cuda").to(torch.bfloat16)
+        dref = dY[:, rows].double() @ What
+        dX = w4.w4a16_linear_grad(dY, p, sc, z, out_dtype=torch.float32)
+        check(dX, dref, (2 * U + N * 2.0 ** -23) * (dY[:, rows].double().abs() @ big), 2 * U,
+              f"gradient of weights past 32 bits M={M}")
+    H, Z = w4.w4a16_gated(X, p, sc, z, act="none", save_preact=True)
+    f = torch.tensor([0, N // 2 - 1], device="cuda")
+    (G, tG), (Up, tU) = [(ref[:, i], tol[:, i]) for i in ([0, 2], [3, 7])]
+    check(Z[:, f], G, tG, U, "gate, weights past 32 bits")
+    check(Z[:, N // 2 + f], Up, tU, U, "up, weights past 32 bits")
+    check(H[:, f], G * Up, G.abs() * tU + Up.abs() * tG + tG * tU + 2.0 ** -23 * (G * Up).abs(), None,
+          "gated, weights past 32 bits")
+    del p, X, Y, H, Z, dY, dX
+    torch.cuda.empty_cache()
+
+
+def test_calls_from_two_threads_on_two_streams(w4):
+    """Two host threads, a stream each, call every kernel at the same time on the same weights:
+    the same bits as one call alone."""
+    import threading
+    F, K = 1000, 1024
+    L = Layer(w4, 2 * F, K)
+    Xs = [L.randn(M, K).to(torch.bfloat16) for M in (1, 5, 24, 64, 150, 400)]
+    dHs = [L.randn(X.shape[0], F).to(torch.bfloat16) for X in Xs]
+
+    def once(X, dH):
+        H, Z = w4.w4a16_gated(X, *L.w, save_preact=True)
+        Y = w4.w4a16_linear(X, *L.w, act="silu")
+        dX, db = w4.w4a16_gated_grad(dH, Z, *L.w, dbias=True)
+        return H, Z, Y, dX, db
+
+    want = [once(X, dH) for X, dH in zip(Xs, dHs)]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(order):
+        try:
+            side = torch.cuda.Stream()
+            with torch.cuda.stream(side):
+                for _ in range(15):
+                    got = [(i, once(Xs[i], dHs[i])) for i in order]
+                    side.synchronize()
+                    wrong.extend(i for i, g in got if not all(torch.equal(a, b) for a, b in zip(g, want[i])))
+        except Exception as e:  # seen by the test
+            wrong.append(e)
+
+    ts = [threading.Thread(target=work, args=(o,)) for o in ([0, 1, 2, 3, 4, 5], [5, 3, 1, 4, 2, 0])]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not wrong, wrong[:3]
+
+
 def test_refusals(w4):
     L = Layer(w4, 256, 256)
     X = L.randn(4, 256).to(torch.bfloat16)

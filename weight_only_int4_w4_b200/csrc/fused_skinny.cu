@@ -150,18 +150,19 @@ __device__ __forceinline__ void skinny_finish(const FusedEpi &e, const float *su
   }
 }
 
-// The largest of `n` fp16 scales.
+// The largest size among `n` fp16 scales.
 __device__ __forceinline__ float max_scale(const uint16_t *p, int n) {
+  constexpr uint32_t kAbs = 0x7FFF7FFFu;
   uint32_t m = 0;
   int i = 0;
   if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0)
 #pragma unroll 4
     for (; i + 8 <= n; i += 8) {
       const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p + i));
-      m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x, v.y), __vmaxu2(v.z, v.w)));
+      m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & kAbs, v.y & kAbs), __vmaxu2(v.z & kAbs, v.w & kAbs)));
     }
   m = max(m >> 16, m & 0xFFFFu);
-  for (; i < n; ++i) m = max(m, (uint32_t)__ldg(p + i));
+  for (; i < n; ++i) m = max(m, (uint32_t)__ldg(p + i) & 0x7FFFu);
   return half_bits_to_float((uint16_t)m);
 }
 

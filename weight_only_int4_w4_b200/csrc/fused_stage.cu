@@ -54,7 +54,7 @@ __device__ __forceinline__ void prep_rows(const uint16_t *scales, const uint16_t
     const int64_t n = n0 + 4 * w + i;
     float mx = 0.0f;
     if (n < N)
-      for (int64_t g = lane; g < kg; g += 32) mx = fmaxf(mx, half_bits_to_float(scales[n * kg + g]));
+      for (int64_t g = lane; g < kg; g += 32) mx = fmaxf(mx, fabsf(half_bits_to_float(scales[n * kg + g])));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
     const float2 f = pow2_to(mx, 10);
