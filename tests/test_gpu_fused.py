@@ -435,6 +435,35 @@ def test_other_stream_shared_workspace_and_graph(w4):
         assert all(torch.equal(a, b) for a, b in zip(out, want))
 
 
+@pytest.mark.parametrize("M", [4, 32, 96])
+def test_results_on_another_stream_are_not_written_over(w4, M):
+    """Kernels still queued on the current stream write memory that they gave back: results on
+    another stream do not lie there."""
+    F = 256
+    L = Layer(w4, 2 * F, 256)
+    X = L.randn(M, 256).to(torch.bfloat16)
+    dH = L.randn(M, F).to(torch.bfloat16)
+
+    def call(stream):
+        H, Z = w4.w4a16_gated(X, *L.w, save_preact=True, stream=stream)
+        Y, Z2 = w4.w4a16_linear(X, *L.w, act="silu", save_preact=True, stream=stream)
+        dX, db = w4.w4a16_gated_grad(dH, Z, *L.w, dbias=True, stream=stream)
+        return H, Z, Y, Z2, dX, db
+
+    want = call(None)
+    side = torch.cuda.Stream()
+    call(side)
+    torch.cuda.synchronize()
+    given_back = [torch.empty_like(t) for t in want]
+    torch.cuda._sleep(40_000_000)  # some 20 ms
+    for t in given_back:
+        t.fill_(7)
+    del given_back, t
+    got = call(side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_offsets_past_32_bits(w4):
     """More than 2^31 output elements: the last tokens' outputs and gradients."""
     M, N, K = 75000, 28704, 64

@@ -400,7 +400,7 @@ def _bad(name, what):
     raise ValueError(f"{name}: {what}")
 
 
-def _fused_layer(name, X, packed, scales, zeros, awq_s, group):
+def _fused_layer(name, X, packed, scales, zeros, awq_s, group, stream):
     """The checks that every fused call shares; returns (device index, M, N, K)."""
     dev = X.get_device()
     if dev < 0 or X.dim() != 2 or X.dtype not in _X_DT or not X.is_contiguous():
@@ -417,6 +417,8 @@ def _fused_layer(name, X, packed, scales, zeros, awq_s, group):
             _bad(name, f"scales and zeros are contiguous fp16 tensors of shape {shape} on the activations' device")
     if awq_s is not None:
         _vector(name, "awq_s", awq_s, K, dev)
+    if stream is not None and stream.device_index != dev:
+        _bad(name, "stream is one of the activations' device")
     return dev, X.shape[0], N, K
 
 
@@ -430,11 +432,20 @@ def _matrix(name, what, t, M, N, dtype, dev):
         _bad(name, f"{what} is a contiguous {dtype} tensor of shape [{M}, {N}] on the activations' device")
 
 
-def _output(name, out, M, N, out_dtype, like, dev):
+def _new(like, shape, dtype, stream):
+    """A result tensor that belongs to the stream that writes it: one of the current stream's might
+    lie where kernels still queued there read or write."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _output(name, out, M, N, out_dtype, like, dev, stream):
     if out is None:
         if out_dtype is not None and out_dtype not in _DT:
             _bad(name, "the output is fp32, fp16 or bf16")
-        return like.new_empty((M, N), dtype=out_dtype)
+        return _new(like, (M, N), out_dtype, stream)
     if out.dtype not in _DT or out_dtype not in (None, out.dtype):
         _bad(name, "out is fp32, fp16 or bf16, and of out_dtype if that is given")
     _matrix(name, "out", out, M, N, out.dtype, dev)
@@ -470,18 +481,19 @@ def w4a16_linear(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, ze
     """Y = act(X . W^T + bias) + residual.  X [M,K] fp16/bf16 (CUDA), bias fp32 [N], residual [M,N] of
     the output's type (`out` may be the residual itself); Y in out_dtype (X's type by default).
     With save_preact, returns (Y, Z), Z = X . W^T + bias in X's type, for w4a16_linear_grad.
+    With `stream`, the call runs there and the results belong to it, as if it were current.
     Tensors that do not fit raise ValueError, what the library refuses raises W4Error."""
     name = "w4a16_linear"
-    dev, M, N, K = _fused_layer(name, X, packed, scales, zeros, awq_s, group)
+    dev, M, N, K = _fused_layer(name, X, packed, scales, zeros, awq_s, group, stream)
     if X.shape[1] != K:
         _bad(name, f"X has {X.shape[1]} channels, the weights {K}")
     a = _act(name, act)
     if bias is not None:
         _vector(name, "bias", bias, N, dev)
-    Y = _output(name, out, M, N, out_dtype, X, dev)
+    Y = _output(name, out, M, N, out_dtype, X, dev, stream)
     if residual is not None:
         _matrix(name, "residual", residual, M, N, Y.dtype, dev)
-    Z = X.new_empty((M, N)) if save_preact else None
+    Z = _new(X, (M, N), None, stream) if save_preact else None
     decode = M <= _DECODE_TOKENS and group == GROUP
     _fused_call(name, _lib.w4a16_linear, None if decode else _lib.w4a16_linear_workspace_size, (M, N, K), dev, ws, stream,
                 (X.data_ptr(), _X_DT[X.dtype], M, N, K, group, packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(),
@@ -499,7 +511,7 @@ def w4a16_gated(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zer
     H [M,F] in out_dtype (X's type by default).  With save_preact, returns (H, Z), Z = [G U]
     [M,2F] in X's type, for w4a16_gated_grad.  Errors as w4a16_linear."""
     name = "w4a16_gated"
-    dev, M, N, K = _fused_layer(name, X, packed, scales, zeros, awq_s, group)
+    dev, M, N, K = _fused_layer(name, X, packed, scales, zeros, awq_s, group, stream)
     if X.shape[1] != K:
         _bad(name, f"X has {X.shape[1]} channels, the weights {K}")
     if N % 2:
@@ -508,8 +520,8 @@ def w4a16_gated(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zer
     if bias is not None:
         _vector(name, "bias", bias, N, dev)
     F = N // 2
-    H = _output(name, out, M, F, out_dtype, X, dev)
-    Z = X.new_empty((M, N)) if save_preact else None
+    H = _output(name, out, M, F, out_dtype, X, dev, stream)
+    Z = _new(X, (M, N), None, stream) if save_preact else None
     decode = M <= _DECODE_TOKENS and group == GROUP
     _fused_call(name, _lib.w4a16_gated, None if decode else _lib.w4a16_gated_workspace_size, (M, F, K), dev, ws, stream,
                 (X.data_ptr(), _X_DT[X.dtype], M, F, K, group, packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(),
@@ -541,7 +553,7 @@ def w4a16_gated_grad(dH: torch.Tensor, preact: torch.Tensor, packed: torch.Tenso
 
 def _grad(name, gated, fn, size_fn, dY, packed, scales, zeros, awq_s, preact, act, dbias, out_dtype, out, group, ws,
           stream):
-    dev, M, N, K = _fused_layer(name, dY, packed, scales, zeros, awq_s, group)
+    dev, M, N, K = _fused_layer(name, dY, packed, scales, zeros, awq_s, group, stream)
     if gated and N % 2:
         _bad(name, "the weights have an even number of rows, gate rows first")
     width = N // 2 if gated else N
@@ -550,8 +562,8 @@ def _grad(name, gated, fn, size_fn, dY, packed, scales, zeros, awq_s, preact, ac
     a = _act(name, act)
     if preact is not None:
         _matrix(name, "preact", preact, M, N, dY.dtype, dev)
-    dX = _output(name, out, M, K, out_dtype, dY, dev)
-    db = dY.new_empty(N, dtype=torch.float32) if dbias else None
+    dX = _output(name, out, M, K, out_dtype, dY, dev, stream)
+    db = _new(dY, (N,), torch.float32, stream) if dbias else None
     _fused_call(name, fn, size_fn, (M, width, K), dev, ws, stream,
                 (dY.data_ptr(), _X_DT[dY.dtype], M, width, K, group, packed.data_ptr(), scales.data_ptr(),
                  zeros.data_ptr(), 0 if awq_s is None else awq_s.data_ptr(), 0 if preact is None else preact.data_ptr(),
