@@ -21,6 +21,11 @@
 // Roles (768 threads): warp 0 loads activations (TMA), warp 1 codes (TMA), warp 2 issues the
 // MMAs, warp 3 owns TMEM, warps 4..7 write results, warps 8..23 convert in four sets that
 // take turns, a group and an A buffer each.
+//
+// Measured with 16 / 48 tokens, staging included, back to back in a graph: 12 / 14 us at
+// 4096 x 4096, 22.9 / 24.8 us at 14336 -> 4096, 31.2 / 32.8 us for the gated 4096 -> 2 x
+// 14336, 98 / 103 us for 8192 -> 2 x 28672 (250 MB, 2.5 TB/s): conversion and its hand-over
+// to the MMAs, about 300 cycles a group, is level with the bytes.
 #include "act.cuh"
 #include "common.cuh"
 

@@ -8,6 +8,11 @@
 //   tokens  e[m] = 2^b with the token's largest |value| * e in [2^13, 2^14).
 // Both are undone in fp32 in the product's epilogue.  bf16 activations convert exactly
 // (8 significant bits); with AWQ, x * s is rounded to fp16 once.
+//
+// Bound: HBM and the latency of a token's largest value, which has to be known before its
+// first store.  Measured: 66 us for 2644 tokens of 17792 and the factors of 12850 rows
+// (216 MB read and written, 3.3 TB/s), 95 us for dZ of 2048 tokens of 2 x 14336 (294 MB,
+// 3.1 TB/s).
 #include "act.cuh"
 #include "common.cuh"
 

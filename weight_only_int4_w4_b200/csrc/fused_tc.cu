@@ -3,16 +3,19 @@
 //   kLinear, kGated   D[n][m] = sum_k W^[n][k] x'[m][k]     (Z = X . W^T)
 //   kGrad             D[k][m] = sum_n W^[n][k] dz'[m][n]    (dX = dZ . W^)
 //
-// One persistent CTA per SM computes tiles of 128 rows x BN tokens.  A gated tile is 64
-// gate rows and the 64 up rows that belong to them, so that act(G) * U is formed in the
-// tile's epilogue and neither G nor U goes to memory (unless they are asked for).
+// Persistent CTA pairs, two SMs each, compute tiles of 256 rows x BN tokens with 256-row
+// MMAs: each CTA dequantizes 128 of the rows and loads half of the tokens' activations.  A
+// CTA's part of a gated tile is 64 gate rows and the 64 up rows that belong to them, so
+// that act(G) * U is formed in the tile's epilogue and neither G nor U goes to memory
+// (unless they are asked for).
 //
-// Roles (640 threads): warp 0 loads activations (TMA), warp 1 loads codes (TMA), warp 2
-// issues the MMAs, warp 3 owns TMEM, warps 4..7 write results, warps 8..19 dequantize in
-// three sets of four that take turns, a 64-deep block each.  The MMA and TMA instructions sit under elect.sync in
-// warp-uniform code: issued from a thread-dependent branch, each one costs the issuing
-// thread about 78 ns for operands moved to uniform registers one by one, whatever its
-// size (measured; 4 x 128x256x16 in 313 ns instead of 280).
+// Roles (768 threads): warp 0 loads activations (TMA), warp 1 loads codes (TMA), warp 2 of
+// the pair's first CTA issues the MMAs, warp 3 owns TMEM, warps 4..7 write results, warps
+// 8..23 dequantize in four sets of four that take turns, a 64-deep block and an A buffer
+// each.  The MMA and TMA instructions sit under elect.sync in warp-uniform code: issued
+// from a thread-dependent branch, each one costs the issuing thread about 78 ns for
+// operands moved to uniform registers one by one, whatever its size (measured; 4 x
+// 128x256x16 in 313 ns instead of 280).
 //
 // Forward, the dequantized weights are the MMA's A operand in tensor memory: a thread
 // owns a row, its TMEM lane.  For the gradient the contraction runs over the rows, and
@@ -24,11 +27,19 @@
 // output's own rounding that was half as much error again.
 //
 // Two accumulators in TMEM alternate between tiles, so a tile's epilogue runs under the
-// next one's products; with BN <= 208 they leave room for three 64-deep A buffers.
+// next one's products; with BN <= 192 they leave room for four 64-deep A buffers.
 //
 // Scheduling: whole waves of tiles first, then the tiles that are left are cut along the
-// contraction into one contiguous range per CTA; the pieces' fp32 partials are summed, in
+// contraction into one contiguous range per pair; the pieces' fp32 partials are summed, in
 // order, by fused_finish, which also runs the epilogue.  No block waits for another.
+//
+// Bound: the tensor pipe, and for long calls the power limit.  Measured, this kernel alone:
+// 190 us for 2048 x 8192 -> 8192 with residual (1450 TFLOP/s), 5.6 ms for the gated 8192 x
+// 8192 -> 2 x 28672 (1370), about 330 us for the gradient of the gated 2048 x 4096 -> 2 x
+// 14336 (1460); single CTAs with 128-row MMAs and three sets took 5 to 10 % more.  The
+// epilogue is bound by instruction fetch: code added to it shows in every call (odd rows'
+// columns spread over the lanes made their stores coalesced and all calls 3 to 12 %
+// slower).
 #include "act.cuh"
 #include "common.cuh"
 
