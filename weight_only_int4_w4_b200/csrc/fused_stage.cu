@@ -174,8 +174,9 @@ __global__ void __launch_bounds__(kStageThreads)
 
 __global__ void __launch_bounds__(kStageThreads)
     fused_prep(const uint16_t *scales, const uint16_t *zeros, int64_t kg, int64_t N, float *rinv, uint32_t *tab) {
-  grid_launch_dependents();
   prep_rows(scales, zeros, kg, N, (int64_t)blockIdx.x * kPrepRows, rinv, tab);
+  grid_launch_dependents();  // only here: clusters that start among these blocks do not pack, and one left over
+                             // takes as long again (twice the time at M = 7355, N = 37373, in every second call)
 }
 
 // dZ of `kVec` consecutive rows n.. of token m (gated: n.. lies on one side of F).
@@ -571,10 +572,6 @@ cudaError_t launch_fused_stage_dz(const void *dY, const void *Z, int dtype, int 
   const int64_t want = fused_dz_grid(M, N, gated, sm);
   *sums = want < most ? want : most;
   cfg.gridDim.y = (unsigned)*sums;
-  // A grid that fills the device starts behind the row factors, not among their blocks: those
-  // keep clusters from packing, and one left over takes as long again (twice the time at M = 7355,
-  // N = 37373, in every second call).
-  at[0].val.programmaticStreamSerializationAllowed = *sums <= most / 2;
   return cudaLaunchKernelEx(&cfg, k, static_cast<const uint16_t *>(dY), static_cast<const uint16_t *>(Z), dtype == 2 ? 1 : 0,
                             act, M, N, ld, (const float *)rinv, dzp, tinv, part);
 }
