@@ -371,13 +371,12 @@ __global__ void __launch_bounds__(dz_threads(kGated, V), dz_per_sm(kGated, V))
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// The same for rows longer than a cluster's slices: one
-// token per block, in two passes (the second finds its inputs in L2); columns N.. up to
-// the row stride `ld` become 0.
+// The same for rows longer than a cluster's slices: one token per block, in two passes (the
+// second finds its inputs in L2); columns N.. up to the row stride `ld` become 0.
 template <bool kGated, int kVec>
 __global__ void __launch_bounds__(512)
     fused_stage_dz_rows(const void *dY, const void *Z, int dtype, int act, int64_t N, int64_t ld, const float *rinv,
-                   uint16_t *dzp, float *tinv) {
+                        uint16_t *dzp, float *tinv) {
   grid_launch_dependents();
   grid_dependency_wait();  // the row factors
   __shared__ float red[16];
