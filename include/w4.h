@@ -415,7 +415,8 @@ typedef enum {
  * once before the product.  A token with an infinity or NaN among its activations
  * gets non-finite or unspecified outputs; other tokens are not affected.
  * Outputs may not overlap inputs (but Y = residual) or each other: refused with
- * W4_ERR_INVALID_ARG.  Results do not depend on the order in which blocks finish.
+ * W4_ERR_INVALID_ARG.  So Y may not be X, not even where X is the residual too.
+ * Results do not depend on the order in which blocks finish.
  */
 w4_status w4a16_linear(const void *X, w4_dtype x_dtype, int64_t M, int64_t N,
                        int64_t K, int group, const uint8_t *packed,

@@ -96,3 +96,14 @@ def test_workspace_sizes(lib):
         fn = getattr(lib, f"w4a16_{f}_workspace_size")
         assert fn(0, 16, 128) == fn(1, 0, 128) == fn(1, 16, 100) == fn(1, 16, 0) == fn(-1, 16, 128) == 0
         assert fn(2048, 14336, 4096) < 2 << 30
+
+
+def test_only_the_residual_itself_may_be_written_in_place(lib):
+    """Y may be the residual.  Another input that lies at the same address is still read while
+    Y is written: refused (a square layer's h += act(h . W^T) in place, for one)."""
+    for kw in (dict(X=R), dict(W=R), dict(S=R), dict(Z0=R), dict(bias=R), dict(awq=R), dict(X=R + 16), dict(ws=R, wsb=MB)):
+        for M in (1, 8, 9, 64, 65):
+            assert linear(lib, **{"Y": R, "M": M, **kw}) == BAD, (kw, M)
+            assert b"overlaps" in lib.w4_last_error(), (kw, M)
+    need = lib.w4a16_linear_workspace_size(9, 256, 256)
+    assert linear(lib, Y=R, M=9, wsb=need - 1) == BAD and b"workspace too small" in lib.w4_last_error()  # no overlap

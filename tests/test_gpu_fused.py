@@ -613,3 +613,15 @@ def test_refusals(w4):
     assert e.value.status == w4.W4_ERR_INVALID_ARG and "workspace" in str(e.value)
     with pytest.raises(w4.W4Error):
         w4.w4a16_linear(X[:0], *L.w)
+
+
+@pytest.mark.parametrize("M", [1, 8, 9, 65])
+def test_in_place_over_the_activations_is_refused(w4, M):
+    """h += h . W^T written over h itself: h is read as X while it is written."""
+    L = Layer(w4, 256, 256)
+    h = L.randn(M, 256).to(torch.bfloat16)
+    keep = h.clone()
+    with pytest.raises(w4.W4Error) as e:
+        w4.w4a16_linear(h, *L.w, residual=h, out=h)
+    assert e.value.status == w4.W4_ERR_INVALID_ARG and "overlaps" in str(e.value)
+    assert torch.equal(h, keep)

@@ -196,9 +196,10 @@ w4_status fused_check(const FusedCall &c) {
   const Buf ins[] = {{c.X, xb}, {c.packed, pb}, {c.scales, sb}, {c.zeros, sb}, {c.awq_s, kb}, {c.bias, nb},
                      {c.residual, rb}, {c.grad ? c.Z : nullptr, zb}, {c.workspace, c.workspace_bytes}};
   const Buf outs[] = {{c.Y, yb}, {c.grad ? nullptr : c.Z, zb}, {c.dbias, nb}};
+  constexpr int kResidual = 6;  // its place in ins; by address, another input that lies there too would pass
   for (const Buf &o : outs)
-    for (const Buf &i : ins)
-      if (overlap(o.p, o.n, i.p, i.n) && !(i.p == c.residual && o.p == c.Y && c.residual == c.Y))
+    for (int i = 0; i < 9; ++i)
+      if (overlap(o.p, o.n, ins[i].p, ins[i].n) && !(i == kResidual && o.p == c.Y && c.residual == c.Y))
         return fail(W4_ERR_INVALID_ARG, "an output overlaps an input or the workspace");
   for (int a = 0; a < 3; ++a)
     for (int b = a + 1; b < 3; ++b)

@@ -479,7 +479,7 @@ def w4a16_linear(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, ze
                  residual: torch.Tensor | None = None, out_dtype=None, out: torch.Tensor | None = None,
                  save_preact: bool = False, group: int = GROUP, ws: torch.Tensor | None = None, stream=None):
     """Y = act(X . W^T + bias) + residual.  X [M,K] fp16/bf16 (CUDA), bias fp32 [N], residual [M,N] of
-    the output's type (`out` may be the residual itself); Y in out_dtype (X's type by default).
+    the output's type (`out` may be the residual itself, but not X); Y in out_dtype (X's type by default).
     With save_preact, returns (Y, Z), Z = X . W^T + bias in X's type, for w4a16_linear_grad.
     With `stream`, the call runs there and the results belong to it, as if it were current.
     Tensors that do not fit raise ValueError, what the library refuses raises W4Error."""
