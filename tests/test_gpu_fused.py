@@ -625,3 +625,31 @@ def test_in_place_over_the_activations_is_refused(w4, M):
         w4.w4a16_linear(h, *L.w, residual=h, out=h)
     assert e.value.status == w4.W4_ERR_INVALID_ARG and "overlaps" in str(e.value)
     assert torch.equal(h, keep)
+
+
+@pytest.mark.parametrize("M", [9, 12, 16, 17, 36, 40, 48, 49, 64])
+@pytest.mark.parametrize("K,tiles,less", [(128, 2, 0), (128, 4, 0), (128, 7, 37), (128, 18, 5), (256, 4, 0), (256, 9, 11),
+                                          (384, 5, 1), (640, 4, 0), (640, 6, 3), (1152, 3, 0)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_small_batches_on_wide_shallow_layers(w4, gated, K, tiles, less, M):
+    """Several tiles to a block's range of rows (148 blocks), each of few groups: the ring of
+    codes goes on across tiles, the accumulators alternate, the places of row factors come
+    round again.  Three runs with nothing between them give the same bits."""
+    N = 148 * 128 * tiles - 2 * less
+    L = Layer(w4, N, K, seed=M)
+    X = L.randn(M, K).to(torch.bfloat16)
+    bias = L.randn(N) * KIN if less else None
+    if gated:
+        runs = [w4.w4a16_gated(X, *L.w, bias=bias, out_dtype=torch.float32) for _ in range(3)]
+    else:
+        runs = [w4.w4a16_linear(X, *L.w, bias=bias, out_dtype=torch.float32) for _ in range(3)]
+    assert w4.w4_device_error() == 0
+    assert torch.equal(runs[0], runs[1]) and torch.equal(runs[0], runs[2])
+    Zr = L.z64(X, bias)
+    tz = L.z_tol(X, Zr, False) + (0 if bias is None else 2.0 ** -20 * bias.abs().double())
+    if not gated:
+        return check(runs[0], Zr, tz, 1.2 * U, f"linear {M} x {K} -> {N}")
+    F = N // 2
+    A, Up, tg, tu = act64(Zr[:, :F], "silu"), Zr[:, F:], tz[:, :F], tz[:, F:]
+    check(runs[0], A * Up, A.abs() * tu + 1.2 * tg * Up.abs() + 1.2 * tg * tu + 2.0 ** -20 * (A * Up).abs(), 3 * U,
+          f"gated {M} x {K} -> 2 x {F}")

@@ -124,7 +124,7 @@ bool fused_skinny_plan(int64_t M, int64_t N, int64_t K, int group, bool gated, i
     const int64_t ranges = std::min<int64_t>(w4::fused_gemv_clusters(cluster, sm), cdiv(out, 8));
     const int64_t rows = cdiv(out, ranges), tiles = cdiv(rows, lim), tile_rows = cdiv(rows, tiles);
     if (tiles > 1 << 20 || tiles * cdiv(Kg, cluster) > 1 << 30 ||
-        w4::fsk::code_stages(p.bn, (int)M, (int)std::min<int64_t>(tiles, 512), cluster) < 3)
+        w4::fsk::code_stages(p.bn, (int)M, (int)std::min<int64_t>(tiles, 512), cluster) < w4::fsk::kMinCodeStages)
       continue;
     const double unit = std::max(kConvert, (double)tile_rows * (gated ? 2 : 1) * 68.0 / kBytesPerCycle);
     const double cost = (double)tiles * (double)cdiv(Kg, cluster) * unit + (cluster > 1 ? kCluster : 0.0);

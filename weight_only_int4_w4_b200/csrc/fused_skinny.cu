@@ -27,6 +27,7 @@
 // 14336, 98 / 103 us for 8192 -> 2 x 28672 (250 MB, 2.5 TB/s): conversion and its hand-over
 // to the MMAs, about 300 cycles a group, is level with the bytes.
 #include "act.cuh"
+#include "code_ring.cuh"
 #include "common.cuh"
 
 namespace w4 {
@@ -43,9 +44,10 @@ struct FusedSkinnyParams {
 
 namespace fsk {
 
-constexpr int kSets = 4, kThreads = 32 * (8 + 4 * kSets);
+constexpr int kThreads = 32 * (8 + 4 * kSets);
 // A stage of codes: 128 rows x 4 groups, as two boxes of 128-byte rows.
-constexpr int kCodeGroups = 4, kCodeBox = 128 * 128, kCodeStage = 2 * kCodeBox;
+constexpr int kCodeBox = 128 * 128, kCodeStage = 2 * kCodeBox;
+static_assert(kCodeGroups == 4, "two boxes of two groups");
 constexpr int kMaxStages = 8, kMaxCodeStages = 5;
 constexpr int kMaxTokens = 64;
 constexpr int kRowFactors = 16;  // tiles whose row factors are kept: conversion may be 8 groups, and so as many
@@ -62,11 +64,6 @@ __host__ __device__ constexpr int fixed_bytes(int bn, int m, int tiles, int clus
 __host__ __device__ constexpr int code_stages(int bn, int m, int tiles, int cluster) {
   const int n = (227 * 1024 - fixed_bytes(bn, m, tiles, cluster)) / kCodeStage;
   return n > kMaxCodeStages ? kMaxCodeStages : n;
-}
-
-__device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n) {
-  asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(smem_u32(bar)), "r"(n)
-               : "memory");
 }
 
 }  // namespace fsk
@@ -202,7 +199,7 @@ __global__ void __launch_bounds__(fsk::kThreads, 1)
     }
     for (int i = 0; i < nc; ++i) {
       mbar_init(&cfull[i], 1);
-      mbar_init(&cempty[i], 128 * kCodeGroups);
+      mbar_init(&cempty[i], 128 * kSets);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&dfull[i], 1);
@@ -303,24 +300,16 @@ __global__ void __launch_bounds__(fsk::kThreads, 1)
     const uint32_t sw = (uint32_t)(r & 7);
     int s = set, ps = 0;
     uint32_t pph = 0, sph = 0;
-    // the group's number in its tile, and its stage of the codes' ring (a tile starts a new one)
-    const int per_tile = (ng + kCodeGroups - 1) / kCodeGroups;
-    int gi = set, cs = 0, at_stage = 0;  // at_stage: cs, counted in the tile
-    uint32_t cph = 0;
-    int tile = -1, next_tile = 0;
+    CodeWalk walk(set, ng, nc);
+    int tile = -1;
     float rf = 0.0f;
     const uint16_t *sp = p.scales, *zp = p.zeros;
     uint32_t scn = 0, zn = 0;
-    for (int i = set; i < total; i += kSets) {
-      while (gi >= ng) {
-        gi -= ng;
-        cs += per_tile - at_stage;
-        at_stage = 0;
-        ++next_tile;
-      }
-      if (next_tile != tile) {
+    for (int i = set; i < total; i += kSets, walk.next()) {
+      const int gi = walk.group;
+      if (walk.tile != tile) {
         // this thread's row of the tile: its factor, and where its constants lie
-        tile = next_tile;
+        tile = walk.tile;
         const int64_t row = tile_row(tile);
         const int rows = (int)(tile_row(tile + 1) - row), f = kGated ? r & 63 : r;
         const int64_t n = row + (f < rows ? f : 0) + (kGated && r >= 64 ? e.N : 0);
@@ -333,12 +322,10 @@ __global__ void __launch_bounds__(fsk::kThreads, 1)
         // (whichever set starts a tile writes the same values)
         sR[(tile % kRowFactors) * 128 + r] = rr.y;
       }
+      if (!walk.reach([&](int c, uint32_t ph) { return ftc::wait_all(&cfull[c], ph, kErrTimeoutDequant); },
+                      [&](int c) { mbar_arrive(&cempty[c]); })) { ok = false; break; }
       const int sub = gi % kCodeGroups;
-      cs += gi / kCodeGroups - at_stage;
-      at_stage = gi / kCodeGroups;
-      while (cs >= nc) cs -= nc, cph ^= 1u;
-      if (!ftc::wait_all(&cfull[cs], cph, kErrTimeoutDequant)) { ok = false; break; }
-      const uint32_t base = smem_u32(sC + cs * kCodeStage + (sub >> 1) * kCodeBox) + (uint32_t)(r * 128);
+      const uint32_t base = smem_u32(sC + walk.slot * kCodeStage + (sub >> 1) * kCodeBox) + (uint32_t)(r * 128);
       const uint32_t c0 = (uint32_t)(4 * (sub & 1));
       ftc::GroupK k;
       {
@@ -370,14 +357,12 @@ __global__ void __launch_bounds__(fsk::kThreads, 1)
       tc_wait_st();
       tc_fence_before();
       mbar_arrive(&full[s]);
-      // a stage that the tile's end cuts short is given back in full by its last group
-      if (gi == ng - 1) mbar_arrive_n(&cempty[cs], (uint32_t)(kCodeGroups - sub));
-      else mbar_arrive(&cempty[cs]);
+      mbar_arrive(&cempty[walk.slot]);
+      walk.leave();
       ps = s;
       pph = sph;
       s += kSets;
       if (s >= NS) s -= NS, sph ^= 1u;
-      gi += kSets;
     }
   } else if (warp >= 4) {
     // ---- results: the tile's sums into shared memory as [token][row], and (without a
