@@ -408,8 +408,10 @@ typedef enum {
  *             need not be zeroed and holds nothing between calls; its first 128
  *             KiB are not touched, so that one buffer may serve w4a16_gemm (whose
  *             counters lie there) and the fused operators in turn.  Calls that
- *             share it must not overlap in time.  With at most 8 tokens and
- *             group 128 none is needed, and NULL may be given.
+ *             share it must not overlap in time, on the device or on the host: a
+ *             call is up to six launches, and those of two host threads may
+ *             alternate, even on one stream.  With at most 8 tokens and group 128
+ *             none is needed, and NULL may be given.
  * Z is accumulated in fp32; bias, activation and residual are applied in fp32 and
  * each output is rounded once.  W^ (and, with awq_s, x * s) may be rounded to fp16
  * once before the product.  A token with an infinity or NaN among its activations

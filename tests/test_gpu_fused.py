@@ -653,3 +653,40 @@ def test_small_batches_on_wide_shallow_layers(w4, gated, K, tiles, less, M):
     A, Up, tg, tu = act64(Zr[:, :F], "silu"), Zr[:, F:], tz[:, :F], tz[:, F:]
     check(runs[0], A * Up, A.abs() * tu + 1.2 * tg * Up.abs() + 1.2 * tg * tu + 2.0 ** -20 * (A * Up).abs(), 3 * U,
           f"gated {M} x {K} -> 2 x {F}")
+
+
+def test_calls_from_threads_on_one_stream(w4):
+    """Three host threads call on the same stream, with the binding's own workspace: the same bits
+    as one call alone."""
+    import threading
+    F, K = 1000, 1024
+    L = Layer(w4, 2 * F, K)
+    Xs = [L.randn(M, K).to(torch.bfloat16) for M in (24, 64, 150, 400)]
+    dHs = [L.randn(X.shape[0], F).to(torch.bfloat16) for X in Xs]
+
+    def once(i):
+        H, Z = w4.w4a16_gated(Xs[i], *L.w, save_preact=True)
+        Y = w4.w4a16_linear(Xs[i], *L.w, act="silu")
+        dX, db = w4.w4a16_gated_grad(dHs[i], Z, *L.w, dbias=True)
+        return H, Z, Y, dX, db
+
+    want = [once(i) for i in range(4)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    wrong = []
+
+    def work(order):
+        try:
+            with torch.cuda.stream(side):
+                for _ in range(25):
+                    got = [(i, once(i)) for i in order]
+                    wrong.extend(i for i, g in got if not all(torch.equal(a, b) for a, b in zip(g, want[i])))
+        except Exception as e:  # seen by the test
+            wrong.append(e)
+
+    ts = [threading.Thread(target=work, args=(o,)) for o in ([0, 1, 2, 3], [3, 2, 1, 0], [1, 3, 0, 2])]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not wrong, wrong[:3]

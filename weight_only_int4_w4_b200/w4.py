@@ -375,6 +375,7 @@ def w4a16_gated_grad_workspace_size(M: int, F: int, K: int) -> int:
 
 
 _fused_ws: dict = {}
+_fused_locks: dict = {}
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _DECODE_TOKENS = 8  # up to here, with groups of 128, a forward call needs no workspace
 _X_DT = {torch.float16: W4_F16, torch.bfloat16: W4_BF16}
@@ -464,9 +465,18 @@ def _fused_call(name, fn, size_fn, sizes, dev, ws, stream, args):
             return _fused_call(name, fn, size_fn, sizes, dev, ws, stream, args)
     raw = _raw_stream(dev) if stream is None else stream.cuda_stream
     if ws is None:
-        if size_fn is not None:
-            need = size_fn(*sizes)
-            ws = _fused_workspace(need, dev, raw, stream) if need else None
+        need = size_fn(*sizes) if size_fn is not None else 0
+        if need:
+            # A call is several launches that hand data on through the cached workspace, and other
+            # threads run during it: one call at a time on a workspace.  (Re-entrant: a finalizer
+            # that runs while it is allocated may make a call of its own.)
+            lock = _fused_locks.get((dev, raw)) or _fused_locks.setdefault((dev, raw), threading.RLock())
+            with lock:
+                ws = _fused_workspace(need, dev, raw, stream)
+                st = fn(*args, ws.data_ptr(), ws.numel(), raw)
+            if st:
+                raise W4Error(st, name)
+            return
     elif ws.dtype is not torch.uint8 or not ws.is_contiguous() or ws.get_device() != dev:
         _bad(name, "ws is a contiguous uint8 tensor on the activations' device")
     st = fn(*args, 0, 0, raw) if ws is None else fn(*args, ws.data_ptr(), ws.numel(), raw)
@@ -482,6 +492,9 @@ def w4a16_linear(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, ze
     the output's type (`out` may be the residual itself, but not X); Y in out_dtype (X's type by default).
     With save_preact, returns (Y, Z), Z = X . W^T + bias in X's type, for w4a16_linear_grad.
     With `stream`, the call runs there and the results belong to it, as if it were current.
+    Without `ws`, the workspace is the binding's own, one per device and stream, and threads may share a
+    stream.  Calls that share a given `ws` must not overlap in time: not on the device, and not on the
+    host either (a call is several launches).
     Tensors that do not fit raise ValueError, what the library refuses raises W4Error."""
     name = "w4a16_linear"
     dev, M, N, K = _fused_layer(name, X, packed, scales, zeros, awq_s, group, stream)
