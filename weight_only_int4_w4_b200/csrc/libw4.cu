@@ -145,8 +145,17 @@ CUresult encode_2d(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap *out, CUte
   const cuuint64_t strides[1] = {stride_bytes};
   const cuuint32_t box[2] = {b0, b1};
   const cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(out, dt, 2, const_cast<void *>(addr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-                   l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  auto encode = [&] {
+    return enc(out, dt, 2, const_cast<void *>(addr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz, l2,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  if (r == CUDA_ERROR_INVALID_CONTEXT) {
+    // This is the first CUDA call of a host thread: launches make the device's context current by
+    // themselves, a driver call does not.  cudaSetDevice does.
+    int dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = encode();
+  }
   if (r != CUDA_SUCCESS) return r;
   const int slot = t_maps.n < kMapCache ? t_maps.n++ : (t_maps.next++ % kMapCache);
   t_maps.key[slot] = k;
