@@ -1,4 +1,5 @@
-"""Calls from host threads: a thread's first CUDA call may be one of the library's."""
+"""Calls from host threads: a thread's first CUDA call may be one of the library's, and several threads
+may call on one stream with the binding's own workspace."""
 import threading
 
 import pytest
@@ -64,3 +65,31 @@ def test_the_first_call_of_a_thread(w4, M):
     torch.cuda.synchronize()
     assert not wrong, wrong
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_calls_from_threads_on_one_stream(w4):
+    """Three threads call every kernel on one stream: the same bits as one call alone."""
+    N, K = 2000, 1024
+    w, gen = layer(w4, N, K, 1)
+    Xs = [torch.randn((M, K), generator=gen, device="cuda").to(torch.bfloat16) for M in (1, 6, 16, 48, 150, 300)]
+    want = [w4.w4a16_gemm(X, *w) for X in Xs]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    wrong = []
+
+    def work(order):
+        try:
+            with torch.cuda.stream(side):
+                for _ in range(40):
+                    got = [(i, w4.w4a16_gemm(Xs[i], *w)) for i in order]
+                    wrong.extend(i for i, g in got if not torch.equal(g, want[i]))
+        except Exception as e:  # seen by the test
+            wrong.append(e)
+
+    ts = [threading.Thread(target=work, args=(o,)) for o in ([0, 1, 2, 3, 4, 5], [5, 4, 3, 2, 1, 0], [2, 5, 3, 0, 4, 1])]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not wrong, wrong[:3]
+    assert w4.w4_device_error() == 0

@@ -3,6 +3,7 @@ replaced by functions that note when they begin and end, and the stream queries 
 stream, so that the threads meet at will."""
 import threading
 import time
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -27,7 +28,7 @@ class Calls:
         self.lock, self.inside, self.most, self.count = threading.Lock(), {}, 0, 0
 
     def __call__(self, *args):
-        ws = args[-3]
+        ws = getattr(args[-3], "value", args[-3])
         with self.lock:
             self.count += 1
             self.inside[ws] = self.inside.get(ws, 0) + 1
@@ -95,3 +96,19 @@ def test_a_call_inside_the_allocation_does_not_wait_for_itself(w4, monkeypatch):
     t.start()
     t.join(20)
     assert not t.is_alive() and calls.count == 2
+
+
+@pytest.mark.parametrize("name", ["w4a16_gemm", "w4a16_gemm_host", "w4a16_gemm_host_async", "w4a16_gemm_outliers"])
+def test_the_plain_product_likewise(w4, monkeypatch, name):
+    """w4a16_gemm and its relatives stage their operand in the cached workspace from 4 tokens on."""
+    calls, ws, t = Calls(), torch.empty(64, dtype=torch.uint8), torch.empty(16, dtype=torch.float32)
+    monkeypatch.setattr(w4._lib, name, calls)
+    monkeypatch.setattr(w4, "workspace", lambda M, N, K, device, stream=None: ws)
+    X = SimpleNamespace(is_cuda=True, dim=lambda: 2, is_contiguous=lambda: True, dtype=torch.bfloat16, shape=(16, 128),
+                        device=torch.device("cuda", 0), data_ptr=lambda: 256)
+    kw = dict(stream=SimpleNamespace(cuda_stream=7))
+    in_threads(3, {"w4a16_gemm": lambda: w4.w4a16_gemm(X, t, t, t, out=t, **kw),
+                   "w4a16_gemm_host": lambda: w4.w4a16_gemm_host(X, X, t, t, t, t, t, **kw),
+                   "w4a16_gemm_host_async": lambda: w4.w4a16_gemm_host(X, X, t, t, t, t, t, wait=False, **kw),
+                   "w4a16_gemm_outliers": lambda: w4.w4a16_gemm_outliers(X, t, t, t, (t, t, t), out=t, **kw)}[name])
+    assert calls.count == 9 and calls.most == 1

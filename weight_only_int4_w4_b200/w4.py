@@ -163,7 +163,9 @@ _ws_cache: dict = {}
 
 def workspace(M: int, N: int, K: int, device, stream=None) -> torch.Tensor | None:
     """A workspace (cached per device and stream) large enough for (M, N, K), zero-filled
-    when allocated.  Every call leaves its counters zero again, so it can be reused."""
+    when allocated.  Every call leaves its counters zero again, so it can be reused.  Calls that
+    are given it as `ws` must not overlap, not even on the host (a call may be several
+    launches); calls without `ws` see to that themselves."""
     need = w4a16_gemm_workspace_size(M, N, K)
     if need == 0:
         return None
@@ -177,6 +179,25 @@ def workspace(M: int, N: int, K: int, device, stream=None) -> torch.Tensor | Non
     return buf
 
 
+_stream_locks: dict = {}
+
+
+def _stream_lock(dev: int, raw: int):
+    """Held from taking a cached workspace until the call's last launch: a call is several launches
+    that hand data on through it, and other threads run during the library's call.  Re-entrant,
+    since a finalizer that runs while the workspace is allocated may make a call of its own."""
+    return _stream_locks.get((dev, raw)) or _stream_locks.setdefault((dev, raw), threading.RLock())
+
+
+def _with_workspace(call, ws, M, N, K, device, stream):
+    """call(ws), with the cached workspace where none is given."""
+    if ws is not None:
+        return call(ws)
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    with _stream_lock(device.index, s.cuda_stream):
+        return call(workspace(M, N, K, device, stream))
+
+
 def w4a16_gemm(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
                awq_s: torch.Tensor | None = None, out_dtype=torch.float32, out: torch.Tensor | None = None,
                ws: torch.Tensor | None = None, group: int = GROUP, stream=None) -> torch.Tensor:
@@ -186,11 +207,10 @@ def w4a16_gemm(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zero
     N = packed.shape[0]
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=X.device)
-    if ws is None:
-        ws = workspace(M, N, K, X.device, stream)
-    _check(_lib.w4a16_gemm(_ptr(X), _DT[X.dtype], M, N, K, group, _ptr(packed), _ptr(scales), _ptr(zeros),
-                           _ptr(awq_s), _ptr(out), _DT[out.dtype], _ptr(ws), 0 if ws is None else ws.numel(),
-                           _stream(stream)), "w4a16_gemm")
+    _check(_with_workspace(
+        lambda w: _lib.w4a16_gemm(_ptr(X), _DT[X.dtype], M, N, K, group, _ptr(packed), _ptr(scales), _ptr(zeros),
+                                  _ptr(awq_s), _ptr(out), _DT[out.dtype], _ptr(w), 0 if w is None else w.numel(),
+                                  _stream(stream)), ws, M, N, K, X.device, stream), "w4a16_gemm")
     return out
 
 
@@ -202,12 +222,12 @@ def w4a16_gemm_host(X_host: torch.Tensor, X_dev: torch.Tensor, packed, scales, z
     (w4a16_gemm_host_async): Y_host is valid after the caller synchronizes the stream."""
     M, K = X_host.shape
     N = packed.shape[0]
-    if ws is None:
-        ws = workspace(M, N, K, X_dev.device, stream)
     fn = _lib.w4a16_gemm_host if wait else _lib.w4a16_gemm_host_async
-    _check(fn(_ptr(X_host), _ptr(X_dev), _DT[X_host.dtype], M, N, K, group, _ptr(packed), _ptr(scales), _ptr(zeros),
-              _ptr(awq_s), _ptr(Y_host), _ptr(Y_dev), _DT[Y_host.dtype], _ptr(ws), 0 if ws is None else ws.numel(),
-              _stream(stream)), "w4a16_gemm_host" if wait else "w4a16_gemm_host_async")
+    _check(_with_workspace(
+        lambda w: fn(_ptr(X_host), _ptr(X_dev), _DT[X_host.dtype], M, N, K, group, _ptr(packed), _ptr(scales),
+                     _ptr(zeros), _ptr(awq_s), _ptr(Y_host), _ptr(Y_dev), _DT[Y_host.dtype], _ptr(w),
+                     0 if w is None else w.numel(), _stream(stream)), ws, M, N, K, X_dev.device, stream),
+           "w4a16_gemm_host" if wait else "w4a16_gemm_host_async")
     return Y_host
 
 
@@ -306,11 +326,11 @@ def w4a16_gemm_outliers(X: torch.Tensor, packed, scales, zeros, csr, awq_s=None,
     row_ptr, col, val = csr
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=X.device)
-    if ws is None:
-        ws = workspace(M, N, K, X.device, stream)
-    _check(_lib.w4a16_gemm_outliers(_ptr(X), _DT[X.dtype], M, N, K, group, _ptr(packed), _ptr(scales), _ptr(zeros),
-                                    _ptr(awq_s), _ptr(row_ptr), _ptr(col), _ptr(val), _ptr(out), _DT[out.dtype],
-                                    _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)), "w4a16_gemm_outliers")
+    _check(_with_workspace(
+        lambda w: _lib.w4a16_gemm_outliers(_ptr(X), _DT[X.dtype], M, N, K, group, _ptr(packed), _ptr(scales),
+                                           _ptr(zeros), _ptr(awq_s), _ptr(row_ptr), _ptr(col), _ptr(val), _ptr(out),
+                                           _DT[out.dtype], _ptr(w), 0 if w is None else w.numel(), _stream(stream)),
+        ws, M, N, K, X.device, stream), "w4a16_gemm_outliers")
     return out
 
 
@@ -375,7 +395,6 @@ def w4a16_gated_grad_workspace_size(M: int, F: int, K: int) -> int:
 
 
 _fused_ws: dict = {}
-_fused_locks: dict = {}
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _DECODE_TOKENS = 8  # up to here, with groups of 128, a forward call needs no workspace
 _X_DT = {torch.float16: W4_F16, torch.bfloat16: W4_BF16}
@@ -467,11 +486,7 @@ def _fused_call(name, fn, size_fn, sizes, dev, ws, stream, args):
     if ws is None:
         need = size_fn(*sizes) if size_fn is not None else 0
         if need:
-            # A call is several launches that hand data on through the cached workspace, and other
-            # threads run during it: one call at a time on a workspace.  (Re-entrant: a finalizer
-            # that runs while it is allocated may make a call of its own.)
-            lock = _fused_locks.get((dev, raw)) or _fused_locks.setdefault((dev, raw), threading.RLock())
-            with lock:
+            with _stream_lock(dev, raw):
                 ws = _fused_workspace(need, dev, raw, stream)
                 st = fn(*args, ws.data_ptr(), ws.numel(), raw)
             if st:
