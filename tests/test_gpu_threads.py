@@ -93,3 +93,25 @@ def test_calls_from_threads_on_one_stream(w4):
         t.join()
     assert not wrong, wrong[:3]
     assert w4.w4_device_error() == 0
+
+
+@pytest.mark.parametrize("M", [1, 16, 100])
+def test_the_first_call_on_another_stream_finds_its_workspace_zeroed(w4, M):
+    """The current stream is busy, and the memory that the new workspace takes was in use."""
+    N, K = 4096, 4096
+    w, gen = layer(w4, N, K, 2)
+    X = torch.randn((M, K), generator=gen, device="cuda").to(torch.bfloat16)
+    want = w4.w4a16_gemm(X, *w)
+    need = max(w4.w4a16_gemm_workspace_size(M, N, K), 1 << 20)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for s in (torch.cuda.current_stream(), side):
+        with torch.cuda.stream(s):
+            torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    out = torch.empty_like(want)
+    torch.cuda._sleep(20_000_000)  # some 10 ms
+    w4.w4a16_gemm(X, *w, out=out, stream=side)
+    side.synchronize()
+    assert w4.w4_device_error() == 0
+    assert torch.equal(out, want)

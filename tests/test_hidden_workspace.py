@@ -112,3 +112,28 @@ def test_the_plain_product_likewise(w4, monkeypatch, name):
                    "w4a16_gemm_host_async": lambda: w4.w4a16_gemm_host(X, X, t, t, t, t, t, wait=False, **kw),
                    "w4a16_gemm_outliers": lambda: w4.w4a16_gemm_outliers(X, t, t, t, (t, t, t), out=t, **kw)}[name])
     assert calls.count == 9 and calls.most == 1
+
+
+def test_the_cached_workspace_is_zeroed_on_the_stream_that_uses_it(w4, monkeypatch):
+    """Zero-filled on the current stream, its counters may not be zero yet when a call on another
+    stream starts (and a buffer that is replaced would go back to the wrong stream)."""
+    on = []
+
+    class Use:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            on.append(self.s)
+
+        def __exit__(self, *a):
+            on.pop()
+
+    monkeypatch.setattr(w4, "_ws_cache", {})
+    monkeypatch.setattr(torch.cuda, "stream", Use)
+    monkeypatch.setattr(w4, "w4a16_gemm_workspace_size", lambda M, N, K: 64)
+    filled = []
+    monkeypatch.setattr(w4.torch, "zeros", lambda n, **kw: filled.append(list(on)) or torch.empty(n, dtype=torch.uint8))
+    side = SimpleNamespace(cuda_stream=9)
+    a = w4.workspace(1, 2, 3, torch.device("cuda", 0), side)
+    assert a is w4.workspace(1, 2, 3, torch.device("cuda", 0), side) and filled == [[side]] and not on

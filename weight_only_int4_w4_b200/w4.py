@@ -174,7 +174,8 @@ def workspace(M: int, N: int, K: int, device, stream=None) -> torch.Tensor | Non
     with _ws_lock:
         buf = _ws_cache.get(key)
         if buf is None or buf.numel() < need:
-            buf = torch.zeros(max(need, 1 << 20), dtype=torch.uint8, device=device)
+            with torch.cuda.stream(s):  # zeroed there before its first use, and given back there
+                buf = torch.zeros(max(need, 1 << 20), dtype=torch.uint8, device=device)
             _ws_cache[key] = buf
     return buf
 
