@@ -75,3 +75,19 @@ def test_one_driver_call_per_larger_size(lib):
 
 def test_a_failed_call_is_made_again(lib):
     assert lib.after_an_error() == 1
+
+
+def test_the_slots_of_two_variants_are_not_mixed_up(tmp_path):
+    """A table [devices][variants] passed by a row would let one variant's slot for a device stand
+    for another variant's: only an array of one slot per device is taken."""
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(build.nvcc_path()))), "include")
+
+    def compiles(dims, arg):
+        (tmp_path / "t.cpp").write_text(f"""#include "smem_attr.cuh"
+            static std::atomic<int> set{dims};
+            int f(int v) {{ return w4::ensure_smem_attr(nullptr, 1, set{arg}); }}""")
+        return subprocess.run(["g++", "-std=c++17", "-fsyntax-only", "-I" + build.SRC_DIR, "-I" + cuda, str(tmp_path / "t.cpp")],
+                              capture_output=True).returncode == 0
+
+    assert compiles("[w4::kAttrDevices]", "") and compiles("[2][w4::kAttrDevices]", "[v]")
+    assert not compiles("[w4::kAttrDevices][2]", "[v]")

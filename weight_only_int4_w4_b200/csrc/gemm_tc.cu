@@ -525,7 +525,7 @@ cudaError_t launch_t(const CUtensorMap &tmX, const CUtensorMap &tmP, const CUten
                      const TcParams &p, cudaStream_t stream) {
   using Cfg = TcCfg<BN>;
   auto kern = p.tail_pieces > 0 ? gemm_tc_kernel<BN, kBf16, kAwq, true> : gemm_tc_kernel<BN, kBf16, kAwq, false>;
-  static std::atomic<int> smem_set[kAttrDevices][2];  // largest size already set, per device and variant
+  static std::atomic<int> smem_set[2][kAttrDevices];  // largest size already set, per variant and device
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), Cfg::kSmem, smem_set[p.tail_pieces > 0]);
   if (e != cudaSuccess) return e;
   dim3 grid((unsigned)((p.N + 127) / 128), (unsigned)((p.M + BN - 1) / BN), (unsigned)p.splits);

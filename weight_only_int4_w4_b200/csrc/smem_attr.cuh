@@ -14,7 +14,7 @@ namespace w4 {
 // two threads at it, a smaller size set last would fail every launch of the larger
 // one, which `set` says is in force.
 constexpr int kAttrDevices = 64;
-inline cudaError_t ensure_smem_attr(const void *func, int bytes, std::atomic<int> *set) {
+inline cudaError_t ensure_smem_attr(const void *func, int bytes, std::atomic<int> (&set)[kAttrDevices]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
