@@ -690,3 +690,45 @@ def test_calls_from_threads_on_one_stream(w4):
     for t in ts:
         t.join()
     assert not wrong, wrong[:3]
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("M", [3, 20, 90])
+def test_activations_of_far_pre_activations(w4, M, act):
+    """Pre-activations up to 2^68, whose square is past fp32, forward, and up to 2^100 in the
+    gradients: an activation is then z or 0 and its slope 1 or 0, never 0 times infinity."""
+    N, K = 192, 256
+    F = N // 2
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(11)
+    W = torch.randn((N, K), generator=gen, device="cuda") * (1.28 / math.sqrt(K))
+    W[F:] *= 2.0 ** -12  # so that act(G) U stays in range
+    L = Layer(w4, N, K, W=W)
+    X = (L.randn(M, K) * 2.0 ** 66).to(torch.bfloat16)
+    Zr = L.z64(X, None)
+    assert float(Zr[:, :F].abs().median()) > 2.0 ** 64
+    tz = L.z_tol(X, Zr, False)
+    Y = w4.w4a16_linear(X, *L.w, act=act, out_dtype=torch.float32)
+    check(Y, act64(Zr, act), 1.2 * tz + 2.0 ** -20 * act64(Zr, act).abs(), 1.2 * U, f"linear {act}")
+    H = w4.w4a16_gated(X, *L.w, act=act, out_dtype=torch.float32)
+    A, Up, tg, tu = act64(Zr[:, :F], act), Zr[:, F:], tz[:, :F], tz[:, F:]
+    check(H, A * Up, A.abs() * tu + 1.2 * tg * Up.abs() + 1.2 * tg * tu + 2.0 ** -20 * (A * Up).abs(), 3 * U, f"gated {act}")
+    Z = L.randn(M, N) * torch.exp2(torch.randint(0, 101, (M, N), generator=gen, device="cuda").float())
+    Z[:, F:] = L.randn(M, F)
+    Z = Z.to(torch.bfloat16)
+    dY = (L.randn(M, N) * 1e-3).to(torch.bfloat16)
+    check_grad(w4, L, dY, Z, act, False, 128, True, torch.float32, f"linear gradient {act}", rel=False)
+    check_grad(w4, L, dY[:, :F].contiguous(), Z, act, True, 128, True, torch.float32, f"gated gradient {act}", rel=False)
+
+
+@pytest.mark.parametrize("gated,N", [(False, 65600), (False, 65537), (True, 2 * 65543)])
+def test_far_pre_activations_of_the_widest_layers(w4, gated, N):
+    """The same in the gradients of layers wider than a cluster's slices."""
+    M, K = 5, 64
+    L = Layer(w4, N, K, group=64, seed=8)
+    Z = L.randn(M, N) * torch.exp2(torch.randint(0, 101, (M, N), generator=L.gen, device="cuda").float())
+    if gated:
+        Z[:, N // 2:] = L.randn(M, N // 2)
+    dY = (L.randn(M, N // 2 if gated else N) * 1e-3).to(torch.bfloat16)
+    for act in ("silu", "gelu_tanh"):
+        check_grad(w4, L, dY, Z.to(torch.bfloat16), act, gated, 64, True, torch.float32, f"wide gradient {gated} {act}", rel=False)

@@ -13,6 +13,9 @@ enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh 
 
 constexpr float kSqrt2OverPi = 0.7978845608028654f;
 constexpr float kGeluCubic = 0.044715f;
+// Bound of 0.044715 x^2 in tanh-GELU's slope: from |x| of some 10 on it is multiplied by 0 (s is 0
+// or 1), which infinity would turn into NaN where x^2 is past fp32.
+constexpr float kCubicMax = 1e30f;
 
 // 1 / (1 + exp(-v)); exp overflows to infinity for v < -88, which gives 0 as it should.
 __device__ __forceinline__ float logistic(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
@@ -44,10 +47,11 @@ __device__ __forceinline__ void act_fwd4(float (&z)[4], int act) {
       z[0] = z[1]; z[1] = z[2]; z[2] = z[3]; z[3] = t;
     }
   } else {
-    // x times the logistic function of x, or of 2 sqrt(2/pi) (x + 0.044715 x^3)
+    // x times the logistic function of x, or of 2 sqrt(2/pi) (x + 0.044715 x^3); b x first, so
+    // that SiLU's 0 never meets an x^2 past fp32
     const float a = act == kActSilu ? 1.0f : 2.0f * kSqrt2OverPi, b = act == kActSilu ? 0.0f : kGeluCubic;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) z[j] *= logistic(a * fmaf(b * z[j], z[j] * z[j], z[j]));
+    for (int j = 0; j < 4; ++j) z[j] *= logistic(a * fmaf(b * z[j] * z[j], z[j], z[j]));
   }
 }
 
@@ -74,7 +78,7 @@ __device__ __forceinline__ void act_both(float x, int act, float &y, float &dy) 
       const float v = 2.0f * kSqrt2OverPi * (x + kGeluCubic * x * x * x);
       const float s = logistic(v);
       y = x * s;
-      dy = s + y * (1.0f - s) * 2.0f * kSqrt2OverPi * (1.0f + 3.0f * kGeluCubic * x * x);
+      dy = s + y * (1.0f - s) * 2.0f * kSqrt2OverPi * (1.0f + 3.0f * fminf(kGeluCubic * x * x, kCubicMax));
       break;
     }
     default:
@@ -94,7 +98,7 @@ __device__ __forceinline__ void act_both8(const float (&x)[8], int act, float (&
     const float a = act == kActSilu ? 1.0f : 2.0f * kSqrt2OverPi, b = act == kActSilu ? 0.0f : kGeluCubic;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float q = b * x[j] * x[j];
+      const float q = fminf(b * x[j] * x[j], kCubicMax);
       const float s = logistic(a * fmaf(q, x[j], x[j]));
       y[j] = x[j] * s;
       dy[j] = fmaf(y[j] * (1.0f - s), a * fmaf(3.0f, q, 1.0f), s);
