@@ -312,7 +312,7 @@ w4_status fused_run_gemv(const FusedCall &c, const GemvFusedPlan &plan, cudaStre
   w4::FusedGemvParams p{};
   p.X = static_cast<const uint16_t *>(c.X);
   p.M = c.M; p.N = c.gated ? c.N / 2 : c.N; p.K = c.K;
-  p.packed = c.packed; p.scales = c.scales; p.zeros = c.zeros; p.awq_s = c.awq_s;
+  p.scales = c.scales; p.zeros = c.zeros; p.awq_s = c.awq_s;
   p.epi.bias = c.bias; p.epi.residual = c.residual; p.epi.Z = c.Z; p.epi.Y = c.Y;
   p.epi.act = (int)c.act; p.epi.z_dtype = (int)c.x_dtype; p.epi.y_dtype = (int)c.y_dtype;
   p.depth = plan.depth;

@@ -44,7 +44,6 @@ namespace w4 {
 struct FusedGemvParams {
   const uint16_t *X;
   int64_t M, N, K;          // N: output columns (F for gated)
-  const uint8_t *packed;
   const uint16_t *scales, *zeros;
   const float *awq_s;
   FusedEpi epi;

@@ -85,10 +85,16 @@ constexpr int kMaxActStages = 8;
 __host__ __device__ constexpr int fixed_bytes(bool grad) {
   return 1024 + kCodeStages * kCodeStage + 2 * kStageOut + (grad ? kSets * kGradAStage : 0) + 256 * 4 + 512;
 }
-__host__ __device__ inline int act_stages(int bn, bool grad) {
+__host__ __device__ constexpr int act_stages(int bn, bool grad) {
   const int n = (227 * 1024 - fixed_bytes(grad)) / (bn * kAct);
   return n > kMaxActStages ? kMaxActStages : n;
 }
+// What the waits by parity rest on.  A set takes every (kSets / 2)-th unit of codes (two blocks
+// each), so it comes back to a code stage at every turn of the ring, and waits for each of
+// the stage's phases.  It waits for the products of its block before last, kSets blocks
+// back, so a stage of activations that it arrives at has been through the turn before.
+static_assert(kSets % 2 == 0 && kCodeStages % (kSets / 2) == 0, "a set visits a code stage at every turn or never");
+static_assert(act_stages(kMaxBn, true) >= kSets && act_stages(kMaxBn, false) >= kSets, "a set's last block is a turn back");
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -523,7 +529,7 @@ __global__ void __launch_bounds__(ftc::kThreads, 1)
       if (d == 0) dph ^= 1u;
     }
   } else if (warp >= 8) {
-    // ---- dequantization: set j takes blocks j, j + 3, ... of the CTA's whole sequence and
+    // ---- dequantization: set j takes blocks j, j + kSets, ... of the CTA's whole sequence and
     // owns A buffer j, so it converts a block while the other sets' blocks are multiplied
     const int set = (warp - 8) >> 2, wq = warp & 3;
     grid_dependency_wait();  // the group constants
