@@ -381,8 +381,8 @@ size_t w4a16_gemm_decode_static_capacity(void);
 /*
  * Fused operators: the layer around the matmul, and its gradients.  The source
  * pages name the fused dequantize-matmul only (ch. 22, section 22.3); these calls
- * take the same weights and put what a transformer block does next into the same
- * kernel, and give the gradients that training adapters over frozen 4-bit
+ * take the same weights and put what a transformer block does next into the
+ * product's epilogue, and give the gradients that training adapters over frozen 4-bit
  * weights needs.  W^ is the [N][K] matrix of the rule above, act is one of:
  */
 typedef enum {
@@ -414,8 +414,10 @@ typedef enum {
  *             none is needed, and NULL may be given.
  * Z is accumulated in fp32; bias, activation and residual are applied in fp32 and
  * each output is rounded once.  W^ (and, with awq_s, x * s) may be rounded to fp16
- * once before the product.  A token with an infinity or NaN among its activations
- * gets non-finite or unspecified outputs; other tokens are not affected.
+ * once before the product; without awq_s, activations below 2^-23 of their token's
+ * largest may lose bits (an error of 2^-34 of that largest at most).  A token with an
+ * infinity or NaN among its activations gets non-finite or unspecified outputs; other
+ * tokens are not affected.
  * Outputs may not overlap inputs (but Y = residual) or each other: refused with
  * W4_ERR_INVALID_ARG.  So Y may not be X, not even where X is the residual too.
  * Results do not depend on the order in which blocks finish.
@@ -429,7 +431,8 @@ w4_status w4a16_linear(const void *X, w4_dtype x_dtype, int64_t M, int64_t N,
                        size_t workspace_bytes, w4_stream_t stream);
 
 /*
- * Gated feed-forward input:  [G U] = X . W^T + bias,  H = act(G) * U, in one kernel.
+ * Gated feed-forward input:  [G U] = X . W^T + bias,  H = act(G) * U.  H is formed in
+ * the product's epilogue: G and U do not go to memory unless Z asks for them.
  *   packed, scales, zeros   of the [2F][K] matrix: F gate rows, then F up rows
  *   bias      device [2F] fp32 or NULL
  *   Z         device [M][2F] of X's type, or NULL: G and U for w4a16_gated_grad

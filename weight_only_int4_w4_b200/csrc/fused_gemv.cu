@@ -23,19 +23,23 @@
 // for codes of 1 (formed once per piece of channels),
 //   sum (q - z) x' = 2^24 (D - z D1).
 // x' = x s 2^b, b per token and piece of channels with the largest |x'| of the piece in
-// [2^13, 2^14): bf16 and fp16 convert exactly, x * s is rounded to fp16 once; 2^-b follows
-// with the scale.
+// [2^13, 2^14): bf16 converts exactly down to 2^-26 and fp16 to 2^-23 of that largest value
+// (of the channels divided by 16; 2^-30 and 2^-27 of the others), below it fp16's subnormals
+// cut bits off; x * s is rounded to fp16 once; 2^-b follows with the scale.
 //
 // Fragments (g = lane / 4, t = lane % 4): lane (g, t) loads the 32 codes of channels
 // 32 t .. 32 t + 31 of rows g and g + 8 of a group; word w of them feeds two MMAs, whose k
 // order is the same permutation on both sides: channels 32 t + 8 w + {0, 4, 1, 5} and
 // {2, 6, 3, 7}.
 //
-// Bound: HBM, and at the start and end of a call latency.  Measured with 1 / 8 tokens, back
-// to back in a graph: 7.0 / 9.4 us at 4096 x 4096 (8.9 MB of weights), 18.2 / 19.5 us at
-// 14336 -> 4096 (31 MB), 22.9 / 25.6 us for the gated 4096 -> 2 x 14336 (62 MB, 2.7 TB/s)
-// and 67.9 / 72.5 us for 8192 -> 2 x 28672 (250 MB, 3.7 TB/s).  A copy ring per lane in
-// place of TMA, and prefetches into L2, were slower.
+// Bound: at the start and end of a call latency; in between neither HBM nor the issue slots:
+// warps wait for loads, the scales and zero points that are fetched one piece ahead among
+// them.  Measured with 1 / 8 tokens, back to back in a graph: 6.8 / 9.1 us at 4096 x 4096
+// (8.9 MB of weights), 18.1 / 19.5 us at 14336 -> 4096 (31 MB), 23.0 / 25.9 us for the gated
+// 4096 -> 2 x 14336 (62 MB, 2.7 TB/s) and 67.9 / 72.5 us for 8192 -> 2 x 28672 (250 MB, 3.7
+// TB/s).  At 62 MB counters give 48 % of the issue slots taken, and the wait for global
+// loads as the largest stall.  A copy ring per lane in place of TMA, and prefetches into
+// L2, were slower.
 #include "act.cuh"
 #include "common.cuh"
 

@@ -22,10 +22,15 @@
 // MMAs, warp 3 owns TMEM, warps 4..7 write results, warps 8..23 convert in four sets that
 // take turns, a group and an A buffer each.
 //
-// Measured with 16 / 48 tokens, staging included, back to back in a graph: 12 / 14 us at
-// 4096 x 4096, 22.9 / 24.8 us at 14336 -> 4096, 31.2 / 32.8 us for the gated 4096 -> 2 x
-// 14336, 98 / 103 us for 8192 -> 2 x 28672 (250 MB, 2.5 TB/s): conversion and its hand-over
-// to the MMAs, about 300 cycles a group, is level with the bytes.
+// Measured with 16 / 48 tokens, staging included, back to back in a graph: 11.9 / 13.8 us at
+// 4096 x 4096, 22.7 / 24.4 us at 14336 -> 4096, 30.7 / 32.2 us for the gated 4096 -> 2 x
+// 14336, 96 / 102 us for 8192 -> 2 x 28672 (250 MB, 2.6 TB/s).  Bound: the converting warps'
+// issue slots, and the start.  At 48 tokens, gated 4096 -> 2 x 14336, counters give 33,100
+// instructions to each of an SM's four schedulers in 53,800 active cycles: some 520 slots
+// for each of a CTA's 64 (tile, group) blocks, waits that poll included, where the bytes of
+// its 98 rows take some 280 cycles of an SM's HBM; the tensor pipe is active for 23 %.  What
+// the other 20,700 cycles are (the first loads, the end, warps that all wait) was not taken
+// apart.
 #include "act.cuh"
 #include "code_ring.cuh"
 #include "common.cuh"

@@ -6,13 +6,17 @@
 //           (q - z) * (scale r) is at most 15 * 2^11 < 65504, and full precision reaches
 //           down to groups whose scale is 2^-24 of the row's largest.
 //   tokens  e[m] = 2^b with the token's largest |value| * e in [2^13, 2^14).
-// Both are undone in fp32 in the product's epilogue.  bf16 activations convert exactly
-// (8 significant bits); with AWQ, x * s is rounded to fp16 once.
+// Both are undone in fp32 in the product's epilogue.  Activations convert exactly down to
+// 2^-30 (bf16, 8 significant bits) or 2^-27 (fp16, 11) of their token's largest, below which
+// fp16's subnormals cut bits off: an error of 2^-38 of the largest at most.  With AWQ, x * s
+// is rounded to fp16 once.
 //
 // Bound: HBM and the latency of a token's largest value, which has to be known before its
 // first store.  Measured: 66 us for 2644 tokens of 17792 and the factors of 12850 rows
-// (216 MB read and written, 3.3 TB/s), 95 us for dZ of 2048 tokens of 2 x 14336 (294 MB,
-// 3.1 TB/s).
+// (216 MB read and written, 3.3 TB/s); 20 us for 2048 tokens of 8192 and the factors of 8192
+// rows (3.4 TB/s of activations); 93 us alone and 104 us in front of the product for dZ of
+// 2048 tokens of 2 x 14336 (294 MB, 2.8 to 3.2 TB/s), where the exchange between a cluster's
+// CTAs (memory barrier and cluster barrier for every token) is what warps wait for most.
 #include "act.cuh"
 #include "common.cuh"
 

@@ -34,9 +34,10 @@
 // order, by fused_finish, which also runs the epilogue.  No block waits for another.
 //
 // Bound: the tensor pipe, and for long calls the power limit.  Measured, this kernel alone:
-// 190 us for 2048 x 8192 -> 8192 with residual (1450 TFLOP/s), 5.6 ms for the gated 8192 x
-// 8192 -> 2 x 28672 (1370), about 330 us for the gradient of the gated 2048 x 4096 -> 2 x
-// 14336 (1460); single CTAs with 128-row MMAs and three sets took 5 to 10 % more.  The
+// 191 us for 2048 x 8192 -> 8192 with residual (1440 TFLOP/s), 5.6 ms for the gated 8192 x
+// 8192 -> 2 x 28672 (1370), 375 us for the gated 2048 x 4096 -> 2 x 14336 with Z saved
+// (1280), 359 us for its gradient (1340), in runs of some 60 calls (the power limit takes
+// more from longer ones); single CTAs with 128-row MMAs and three sets took 5 to 10 % more.  The
 // epilogue is bound by instruction fetch: code added to it shows in every call (odd rows'
 // columns spread over the lanes made their stores coalesced and all calls 3 to 12 %
 // slower).
