@@ -190,10 +190,8 @@ def _stream_lock(dev: int, raw: int):
     return _stream_locks.get((dev, raw)) or _stream_locks.setdefault((dev, raw), threading.RLock())
 
 
-def _with_workspace(call, ws, M, N, K, device, stream):
-    """call(ws), with the cached workspace where none is given."""
-    if ws is not None:
-        return call(ws)
+def _own_workspace(call, M, N, K, device, stream):
+    """call(ws) with the cached workspace, one call at a time on it."""
     s = stream if stream is not None else torch.cuda.current_stream(device)
     with _stream_lock(device.index, s.cuda_stream):
         return call(workspace(M, N, K, device, stream))
@@ -208,10 +206,12 @@ def w4a16_gemm(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zero
     N = packed.shape[0]
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=X.device)
-    _check(_with_workspace(
-        lambda w: _lib.w4a16_gemm(_ptr(X), _DT[X.dtype], M, N, K, group, _ptr(packed), _ptr(scales), _ptr(zeros),
-                                  _ptr(awq_s), _ptr(out), _DT[out.dtype], _ptr(w), 0 if w is None else w.numel(),
-                                  _stream(stream)), ws, M, N, K, X.device, stream), "w4a16_gemm")
+    if ws is None and w4a16_gemm_workspace_size(M, N, K):
+        return _own_workspace(lambda w: w4a16_gemm(X, packed, scales, zeros, awq_s, out=out, ws=w, group=group,
+                                                   stream=stream), M, N, K, X.device, stream)
+    _check(_lib.w4a16_gemm(_ptr(X), _DT[X.dtype], M, N, K, group, _ptr(packed), _ptr(scales), _ptr(zeros),
+                           _ptr(awq_s), _ptr(out), _DT[out.dtype], _ptr(ws), 0 if ws is None else ws.numel(),
+                           _stream(stream)), "w4a16_gemm")
     return out
 
 
@@ -223,12 +223,13 @@ def w4a16_gemm_host(X_host: torch.Tensor, X_dev: torch.Tensor, packed, scales, z
     (w4a16_gemm_host_async): Y_host is valid after the caller synchronizes the stream."""
     M, K = X_host.shape
     N = packed.shape[0]
+    if ws is None and w4a16_gemm_workspace_size(M, N, K):
+        return _own_workspace(lambda w: w4a16_gemm_host(X_host, X_dev, packed, scales, zeros, Y_host, Y_dev, awq_s, w,
+                                                        group, stream, wait), M, N, K, X_dev.device, stream)
     fn = _lib.w4a16_gemm_host if wait else _lib.w4a16_gemm_host_async
-    _check(_with_workspace(
-        lambda w: fn(_ptr(X_host), _ptr(X_dev), _DT[X_host.dtype], M, N, K, group, _ptr(packed), _ptr(scales),
-                     _ptr(zeros), _ptr(awq_s), _ptr(Y_host), _ptr(Y_dev), _DT[Y_host.dtype], _ptr(w),
-                     0 if w is None else w.numel(), _stream(stream)), ws, M, N, K, X_dev.device, stream),
-           "w4a16_gemm_host" if wait else "w4a16_gemm_host_async")
+    _check(fn(_ptr(X_host), _ptr(X_dev), _DT[X_host.dtype], M, N, K, group, _ptr(packed), _ptr(scales), _ptr(zeros),
+              _ptr(awq_s), _ptr(Y_host), _ptr(Y_dev), _DT[Y_host.dtype], _ptr(ws), 0 if ws is None else ws.numel(),
+              _stream(stream)), "w4a16_gemm_host" if wait else "w4a16_gemm_host_async")
     return Y_host
 
 
@@ -327,11 +328,12 @@ def w4a16_gemm_outliers(X: torch.Tensor, packed, scales, zeros, csr, awq_s=None,
     row_ptr, col, val = csr
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=X.device)
-    _check(_with_workspace(
-        lambda w: _lib.w4a16_gemm_outliers(_ptr(X), _DT[X.dtype], M, N, K, group, _ptr(packed), _ptr(scales),
-                                           _ptr(zeros), _ptr(awq_s), _ptr(row_ptr), _ptr(col), _ptr(val), _ptr(out),
-                                           _DT[out.dtype], _ptr(w), 0 if w is None else w.numel(), _stream(stream)),
-        ws, M, N, K, X.device, stream), "w4a16_gemm_outliers")
+    if ws is None and w4a16_gemm_workspace_size(M, N, K):
+        return _own_workspace(lambda w: w4a16_gemm_outliers(X, packed, scales, zeros, csr, awq_s, out=out, ws=w, group=group,
+                                                            stream=stream), M, N, K, X.device, stream)
+    _check(_lib.w4a16_gemm_outliers(_ptr(X), _DT[X.dtype], M, N, K, group, _ptr(packed), _ptr(scales), _ptr(zeros),
+                                    _ptr(awq_s), _ptr(row_ptr), _ptr(col), _ptr(val), _ptr(out), _DT[out.dtype],
+                                    _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)), "w4a16_gemm_outliers")
     return out
 
 
