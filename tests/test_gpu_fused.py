@@ -732,3 +732,62 @@ def test_far_pre_activations_of_the_widest_layers(w4, gated, N):
     dY = (L.randn(M, N // 2 if gated else N) * 1e-3).to(torch.bfloat16)
     for act in ("silu", "gelu_tanh"):
         check_grad(w4, L, dY, Z.to(torch.bfloat16), act, gated, 64, True, torch.float32, f"wide gradient {gated} {act}", rel=False)
+
+
+@pytest.mark.parametrize("M", [1, 8, 9, 33, 64, 65])
+@pytest.mark.parametrize("N,K,group", [(1, 128, 128), (2, 256, 128), (3, 64, 32), (7, 384, 128), (9, 128, 64), (17, 128, 128),
+                                       (4096, 14336, 128)])
+def test_narrow_and_deep_layers(w4, M, N, K, group):
+    """A handful of outputs, or clusters that share a range of rows with several tiles: every
+    operator, with residual in place, biases and saved pre-activations."""
+    L = Layer(w4, 2 * N if N < 4096 else N, K, group, seed=M)
+    F = L.N // 2
+    X = L.randn(M, K).to(torch.bfloat16)
+    bias = L.randn(L.N) * KIN
+    Zr = L.z64(X, bias)
+    tz = L.z_tol(X, Zr, False) + 2.0 ** -20 * bias.abs().double()
+    R = L.randn(M, L.N)
+    keep = R.double()
+    Y, Z = w4.w4a16_linear(X, *L.w, bias=bias, act="gelu", residual=R, out=R, save_preact=True, group=group)
+    Yr = act64(Zr, "gelu") + keep
+    check(Y, Yr, 1.2 * tz + 2.0 ** -20 * act64(Zr, "gelu").abs() + 2.0 ** -23 * keep.abs(), None, "linear")
+    check(Z, Zr, tz, None, "linear preact")
+    H, Z = w4.w4a16_gated(X, *L.w, bias=bias, save_preact=True, group=group)
+    A, Up, tg, tu = act64(Zr[:, :F], "silu"), Zr[:, F:], tz[:, :F], tz[:, F:]
+    check(H, A * Up, A.abs() * tu + 1.2 * tg * Up.abs() + 1.2 * tg * tu + 2.0 ** -20 * (A * Up).abs(), None, "gated")
+    check(Z, Zr, tz, None, "gated preact")
+    dY = L.randn(M, L.N).to(torch.bfloat16)
+    check_grad(w4, L, dY, Z, "gelu_tanh", False, group, True, torch.float32, "linear gradient")
+    check_grad(w4, L, dY[:, :F].contiguous(), Z, "silu", True, group, True, torch.bfloat16, "gated gradient")
+
+
+@pytest.mark.parametrize("M", [4, 40, 120])
+def test_two_graphs_replayed_at_the_same_time(w4, M):
+    """Graphs of the same calls on two streams, replayed together: each has a workspace of its own."""
+    F, K = 1000, 2048
+    L = Layer(w4, 2 * F, K)
+    graphs = []
+    for i in range(2):
+        X = L.randn(M, K).to(torch.bfloat16)
+        dH = L.randn(M, F).to(torch.bfloat16)
+
+        def calls():
+            H, Z = w4.w4a16_gated(X, *L.w, save_preact=True)
+            Y = w4.w4a16_linear(X, *L.w, act="silu")
+            dX, db = w4.w4a16_gated_grad(dH, Z, *L.w, dbias=True)
+            return H, Z, Y, dX, db
+
+        want = calls()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = calls()
+        graphs.append((g, out, want, torch.cuda.Stream(), (X, dH)))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for g, _, _, s, _ in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for _, out, want, _, _ in graphs:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    assert w4.w4_device_error() == 0
